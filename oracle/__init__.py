@@ -37,6 +37,8 @@ section; "the pages" are the five web pages on GPTQ this path is built from):
 * ``w4a16`` -- inference with the exported weights: dequantize to the
   activations' 16-bit format and multiply ("GPTQ: Mathematical Foundations
   ...", Inference Execution and Modern Kernel Architectures).
+* ``fp8`` -- block-scaled e4m3 matrices: quantizer, norm, product, gated
+  projection (the format's own definitions; no page covers them).
 * ``metrics`` -- layer output error, brute-force optimum on tiny layers, and
   the loss identity that follows from the OBS error penalty.
 
@@ -54,4 +56,5 @@ from .gptq import gptq_sweep, gptq_layer, FollowReport  # noqa: F401
 from .obs import obs_sequential  # noqa: F401
 from .obq import obq_row, obq_layer  # noqa: F401
 from . import w4a16  # noqa: F401
+from . import fp8  # noqa: F401
 from .metrics import layer_error, layer_error_rows, brute_force_row, loss_identity_rhs  # noqa: F401

@@ -16,6 +16,9 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_NOT_SPD, ERR_WORKSPACE, ERR_HIP, ERR_I
 F32, BF16, F16 = 0, 1, 2
 # workspace kinds
 WS_HESSIAN, WS_PREPARE, WS_QUANTIZE, WS_OBQ, WS_W4A16, WS_LAYER = 0, 1, 2, 3, 4, 5
+WS_FP8_GEMM, WS_FP8_GATED = 6, 7
+# gptq_activation
+ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2
 
 EXPORTS = (
     "gptq_workspace_bytes",
@@ -31,6 +34,10 @@ EXPORTS = (
     "gptq_obq_layer",
     "gptq_export",
     "gptq_w4a16_gemm",
+    "gptq_fp8_quantize",
+    "gptq_rmsnorm_fp8",
+    "gptq_fp8_gemm",
+    "gptq_fp8_gated_gemm",
     "gptq_timing",
     "gptq_timing_read",
     "gptq_last_error",
@@ -146,6 +153,17 @@ def lib() -> ctypes.CDLL:
     L.gptq_w4a16_gemm.argtypes = [_vp, _int, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _int,
                                   _i64, _i64, _vp, _i64, _vp, _sz, _vp]
     L.gptq_w4a16_gemm.restype = _int
+    L.gptq_fp8_quantize.argtypes = [_vp, _int, _i64, _i64, _i64, _int, _vp, _i64, _vp, _vp]
+    L.gptq_fp8_quantize.restype = _int
+    L.gptq_rmsnorm_fp8.argtypes = [_vp, _i64, _vp, _i64, _int, _vp, _int, _i64, _i64,
+                                   ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp]
+    L.gptq_rmsnorm_fp8.restype = _int
+    L.gptq_fp8_gemm.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _int, _i64,
+                                _vp, _sz, _vp]
+    L.gptq_fp8_gemm.restype = _int
+    L.gptq_fp8_gated_gemm.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
+                                      _i64, _int, _vp, _int, _i64, _vp, _i64, _vp, _vp, _sz, _vp]
+    L.gptq_fp8_gated_gemm.restype = _int
     L.gptq_timing.argtypes = [_int]
     L.gptq_timing.restype = _int
     L.gptq_timing_read.argtypes = [ctypes.POINTER(ctypes.c_float), _int]

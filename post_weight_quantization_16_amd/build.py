@@ -31,6 +31,8 @@ SOURCES = [
     ("obq.hip", "obq.o", []),
     ("timing.hip", "timing.o", []),
     ("w4a16.hip", "w4a16.o", []),
+    ("fp8_quant.hip", "fp8_quant.o", []),
+    ("fp8_gemm.hip", "fp8_gemm.o", []),
 ] + [("sweep.hip", f"sweep_g{g}.o", [f"-DGQ_SWEEP_G={g}"]) for g in (0, 32, 64, 128)]
 
 FLAGS = [

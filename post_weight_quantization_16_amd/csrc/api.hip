@@ -116,6 +116,18 @@ JobStreams* job_streams(int dev) {
   return js;
 }
 
+// Shape of a rows x cols operand of the 8-bit calls.
+int check_fp8_shape(int64_t rows, int64_t cols, const char* rn, const char* cn) {
+  if (rows < 0 || rows > kMaxDout)
+    return fail(GPTQ_ERR_INVALID_ARG, "%s must be in [0, %lld]", rn, (long long)kMaxDout);
+  if (cols <= 0 || cols > kMaxDin)
+    return fail(GPTQ_ERR_INVALID_ARG, "%s must be in [1, %lld]", cn, (long long)kMaxDin);
+  return GPTQ_OK;
+}
+// Element pointers must be aligned to their type (the calls that take any
+// byte address say so).
+bool misaligned(const void* p, int dt) { return (uintptr_t)p % (dt == GPTQ_F32 ? 4 : 2) != 0; }
+
 }  // namespace
 
 namespace {
@@ -214,6 +226,12 @@ size_t gptq_workspace_bytes(int which, int64_t d_out, int64_t d_in, int64_t n_to
     case GPTQ_WS_W4A16:   // d_out = N, d_in = K, n_tok = M
       if (d_out <= 0 || d_out > kMaxDout || n_tok <= 0 || n_tok > kMaxDout) return 0;
       return gq::w4a16_ws_bytes(n_tok, d_out, d_in);
+    case GPTQ_WS_FP8_GEMM:
+    case GPTQ_WS_FP8_GATED:
+      if (d_out <= 0 || d_out > kMaxDout || n_tok < 0 || n_tok > kMaxDout) return 0;
+      if (n_tok == 0) return 256;
+      return which == GPTQ_WS_FP8_GEMM ? gq::fp8_gemm_ws_bytes(n_tok, d_out, d_in)
+                                       : gq::fp8_gated_ws_bytes(n_tok, d_out, d_in);
     default:
       return 0;
   }
@@ -504,6 +522,113 @@ int gptq_w4a16_gemm(const void* A, int a_dtype, int64_t M, int64_t K, int64_t ld
   hipError_t e = gq::w4a16_launch(A, a_dtype, M, K, lda, qweight, bits, scales_f16, zeros_f16,
                                   g_idx, g, n_groups, N, C, ldc, ws, ws_bytes, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail("w4a16_gemm", e);
+  return GPTQ_OK;
+}
+
+int gptq_fp8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                      int block_rows, uint8_t* codes, int64_t ld_codes, float* scales,
+                      gptq_stream stream) {
+  int rc = check_fp8_shape(rows, cols, "rows", "cols");
+  if (rc) return rc;
+  if (!valid_dtype(x_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown x_dtype %d", x_dtype);
+  if (block_rows != 1 && block_rows != 128)
+    return fail(GPTQ_ERR_INVALID_ARG, "block_rows must be 1 or 128 (got %d)", block_rows);
+  if (ld_x < cols || ld_codes < cols)
+    return fail(GPTQ_ERR_INVALID_ARG, "ld_x < cols or ld_codes < cols");
+  if (rows == 0) return GPTQ_OK;
+  if (!X || !codes || !scales)
+    return fail(GPTQ_ERR_INVALID_ARG, "X, codes and scales must not be NULL");
+  if (misaligned(X, x_dtype) || misaligned(scales, GPTQ_F32))
+    return fail(GPTQ_ERR_INVALID_ARG, "X and scales must be aligned to their types");
+  hipError_t e = gq::fp8_quantize_launch(X, x_dtype, rows, cols, ld_x, block_rows, codes, ld_codes,
+                                         scales, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail("fp8_quantize", e);
+  return GPTQ_OK;
+}
+
+int gptq_rmsnorm_fp8(const void* X, int64_t ld_x, const void* R, int64_t ld_r, int x_dtype,
+                     const void* gamma, int g_dtype, int64_t rows, int64_t cols, float eps,
+                     void* H, int64_t ld_h, void* Y, int64_t ld_y, uint8_t* codes,
+                     int64_t ld_codes, float* scales, gptq_stream stream) {
+  int rc = check_fp8_shape(rows, cols, "rows", "cols");
+  if (rc) return rc;
+  if (!valid_dtype(x_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown x_dtype %d", x_dtype);
+  if (g_dtype != x_dtype && g_dtype != GPTQ_F32)
+    return fail(GPTQ_ERR_INVALID_ARG, "g_dtype must be x_dtype or GPTQ_F32");
+  if (!(eps >= 0.f) || !std::isfinite(eps))
+    return fail(GPTQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (ld_x < cols || (R && ld_r < cols) || (H && ld_h < cols) || (Y && ld_y < cols) ||
+      (codes && ld_codes < cols))
+    return fail(GPTQ_ERR_INVALID_ARG, "a row stride is smaller than cols");
+  if (rows == 0) return GPTQ_OK;
+  if (!X || !gamma) return fail(GPTQ_ERR_INVALID_ARG, "X and gamma must not be NULL");
+  if (!codes != !scales)
+    return fail(GPTQ_ERR_INVALID_ARG, "codes and scales go together");
+  if (!codes && !Y) return fail(GPTQ_ERR_INVALID_ARG, "codes and Y must not both be NULL");
+  if ((H == X && ld_h != ld_x) || (H && H == R && ld_h != ld_r))
+    return fail(GPTQ_ERR_INVALID_ARG, "H in the place of an input needs its row stride");
+  if (Y && (Y == X || Y == R || Y == H))
+    return fail(GPTQ_ERR_INVALID_ARG, "Y must not overlap X, R or H");
+  if (misaligned(X, x_dtype) || misaligned(R, x_dtype) || misaligned(H, x_dtype) ||
+      misaligned(Y, x_dtype) || misaligned(gamma, g_dtype) || misaligned(scales, GPTQ_F32))
+    return fail(GPTQ_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+  hipError_t e = gq::rmsnorm_fp8_launch(X, ld_x, R, ld_r, x_dtype, gamma, g_dtype, rows, cols, eps,
+                                        H, ld_h, Y, ld_y, codes, ld_codes, scales,
+                                        (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail("rmsnorm_fp8", e);
+  return GPTQ_OK;
+}
+
+int gptq_fp8_gemm(const uint8_t* A, const float* a_scales, int64_t M, int64_t K, int64_t lda,
+                  const uint8_t* B, const float* b_scales, int64_t N, int64_t ldb, void* C,
+                  int c_dtype, int64_t ldc, void* ws, size_t ws_bytes, gptq_stream stream) {
+  int rc = check_fp8_shape(M, K, "M", "K");
+  if (rc) return rc;
+  if (N <= 0 || N > kMaxDout)
+    return fail(GPTQ_ERR_INVALID_ARG, "N must be in [1, %lld]", (long long)kMaxDout);
+  if (!valid_dtype(c_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown c_dtype %d", c_dtype);
+  if (lda < K || ldb < K || ldc < N)
+    return fail(GPTQ_ERR_INVALID_ARG, "lda < K, ldb < K or ldc < N");
+  if (M == 0) return GPTQ_OK;
+  if (!A || !a_scales || !B || !b_scales || !C)
+    return fail(GPTQ_ERR_INVALID_ARG, "A, B, their scales and C must not be NULL");
+  if (misaligned(a_scales, GPTQ_F32) || misaligned(b_scales, GPTQ_F32) || misaligned(C, c_dtype))
+    return fail(GPTQ_ERR_INVALID_ARG, "the scales and C must be aligned to their types");
+  if (ws && (rc = check_ws(ws, ws_bytes, gq::fp8_gemm_ws_bytes(M, N, K), "fp8_gemm"))) return rc;
+  hipError_t e = gq::fp8_gemm_launch(A, a_scales, M, K, lda, B, b_scales, N, ldb, C, c_dtype, ldc,
+                                     ws, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail("fp8_gemm", e);
+  return GPTQ_OK;
+}
+
+int gptq_fp8_gated_gemm(const uint8_t* A, const float* a_scales, int64_t M, int64_t K, int64_t lda,
+                        const uint8_t* G, const float* g_scales, int64_t ldg, const uint8_t* U,
+                        const float* u_scales, int64_t ldu, int64_t N, int activation, void* C,
+                        int c_dtype, int64_t ldc, uint8_t* codes, int64_t ld_codes, float* scales,
+                        void* ws, size_t ws_bytes, gptq_stream stream) {
+  int rc = check_fp8_shape(M, K, "M", "K");
+  if (rc) return rc;
+  if (N <= 0 || N > kMaxDout)
+    return fail(GPTQ_ERR_INVALID_ARG, "N must be in [1, %lld]", (long long)kMaxDout);
+  if (activation < GPTQ_ACT_SILU || activation > GPTQ_ACT_GELU_TANH)
+    return fail(GPTQ_ERR_INVALID_ARG, "unknown activation %d", activation);
+  if (C && !valid_dtype(c_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown c_dtype %d", c_dtype);
+  if (lda < K || ldg < K || ldu < K || (C && ldc < N) || (codes && ld_codes < N))
+    return fail(GPTQ_ERR_INVALID_ARG, "a row stride is smaller than its row");
+  if (M == 0) return GPTQ_OK;
+  if (!A || !a_scales || !G || !g_scales || !U || !u_scales)
+    return fail(GPTQ_ERR_INVALID_ARG, "A, G, U and their scales must not be NULL");
+  if (!codes != !scales) return fail(GPTQ_ERR_INVALID_ARG, "codes and scales go together");
+  if (!C == !codes) return fail(GPTQ_ERR_INVALID_ARG, "give C or codes, one of the two");
+  if (misaligned(a_scales, GPTQ_F32) || misaligned(g_scales, GPTQ_F32) ||
+      misaligned(u_scales, GPTQ_F32) || misaligned(scales, GPTQ_F32) || misaligned(C, c_dtype))
+    return fail(GPTQ_ERR_INVALID_ARG, "the scales and C must be aligned to their types");
+  if (ws && (rc = check_ws(ws, ws_bytes, gq::fp8_gated_ws_bytes(M, N, K), "fp8_gated_gemm")))
+    return rc;
+  hipError_t e = gq::fp8_gated_launch(A, a_scales, M, K, lda, G, g_scales, ldg, U, u_scales, ldu, N,
+                                      activation, C, c_dtype, ldc, codes, ld_codes, scales, ws,
+                                      (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail("fp8_gated_gemm", e);
   return GPTQ_OK;
 }
 

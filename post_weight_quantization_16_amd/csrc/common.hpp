@@ -158,6 +158,25 @@ hipError_t w4a16_launch(const void* A, int a_dtype, int64_t M, int64_t K, int64_
                         int64_t ldc, void* ws, size_t ws_bytes, hipStream_t s);
 size_t w4a16_ws_bytes(int64_t M, int64_t N, int64_t K);
 
+// ---------------------------------------------------------------- 8-bit floating point
+hipError_t fp8_quantize_launch(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld_x,
+                               int block_rows, uint8_t* codes, int64_t ld_c, float* scales,
+                               hipStream_t s);
+hipError_t rmsnorm_fp8_launch(const void* X, int64_t ld_x, const void* R, int64_t ld_r, int dt,
+                              const void* gamma, int g_dt, int64_t rows, int64_t cols, float eps,
+                              void* S, int64_t ld_s, void* Y, int64_t ld_y, uint8_t* codes,
+                              int64_t ld_c, float* scales, hipStream_t s);
+size_t fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
+size_t fp8_gated_ws_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t fp8_gemm_launch(const uint8_t* A, const float* sa, int64_t M, int64_t K, int64_t lda,
+                           const uint8_t* B, const float* sb, int64_t N, int64_t ldb, void* C,
+                           int c_dt, int64_t ldc, void* ws, hipStream_t s);
+hipError_t fp8_gated_launch(const uint8_t* A, const float* sa, int64_t M, int64_t K, int64_t lda,
+                            const uint8_t* G, const float* sg, int64_t ldg, const uint8_t* U,
+                            const float* su, int64_t ldu, int64_t N, int act, void* C, int c_dt,
+                            int64_t ldc, uint8_t* codes, int64_t ld_codes, float* sc, void* ws,
+                            hipStream_t s);
+
 // ---------------------------------------------------------------- export
 hipError_t export_launch(int bits, int64_t m, int64_t d, int64_t ng, const uint32_t* qweight,
                          const float* scales, const uint8_t* zeros, uint32_t* qdense,

@@ -1,0 +1,129 @@
+// Block-scaled e4m3 matrices: device helpers shared by the 8-bit kernels.
+//
+// A value is code·scale, the code in e4m3 (bias 7, three mantissa bits, no
+// infinities, largest 448), the scale fp32 for each block of 128 columns and
+// 1 or 128 rows: s = max(fl32(amax/448), 2^-126), code = e4m3 nearest to x/s,
+// ties to even.  448 reaches the last code, so nothing saturates; the lower
+// limit keeps s normal (an all-zero block gets zero codes).  A block that
+// holds a NaN or an infinity gets s = NaN and NaN codes, so whatever is
+// computed from it is NaN.
+#pragma once
+
+#include "common.hpp"
+
+namespace gq {
+
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+typedef __attribute__((ext_vector_type(8))) int i32x8;
+
+constexpr int kFp8Block = 128;        // columns of a block (and rows, for weights)
+constexpr float kE4m3Max = 448.f;
+
+// Scale of a block from its largest magnitude (NaN or infinite: NaN).
+__device__ __forceinline__ float e4m3_scale(double amax) {
+  const float s = fmaxf((float)(amax / 448.0), 1.17549435e-38f);
+  return __builtin_isfinite(amax) ? s : __builtin_nanf("");
+}
+
+// x/s as a float that rounds to e4m3 as the exact quotient does: the quotient
+// in fp64 (inv = 1/s; one Newton step makes it the correctly rounded one, so
+// exact ties stay ties), its last 32 bits folded into a sticky bit above
+// them, which leaves a value fp32 holds exactly and keeps the side of every
+// border.  fp32 alone would move about one code in 10^6 over a border.
+__device__ __forceinline__ float e4m3_quotient(double x, double s, double inv) {
+  double q = x * inv;
+  q = __builtin_fma(__builtin_fma(-q, s, x), inv, q);
+  uint64_t b = __builtin_bit_cast(uint64_t, q);
+  const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32) | (lo < 1u ? lo : 1u);
+  return (float)__builtin_bit_cast(double, (uint64_t)hi << 32);
+}
+
+// Four floats to four e4m3 codes, byte i from argument i (round to nearest
+// even; NaN stays NaN; |x| <= 464 assumed).
+__device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+}
+
+// Maximum over the 16 lanes of a DPP row (every lane gets it).
+template <int CTRL> __device__ __forceinline__ float dpp_f(float x) {
+  const int v = __builtin_bit_cast(int, x);
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false));
+}
+template <int CTRL> __device__ __forceinline__ double dpp_d(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const int lo = (int)(uint32_t)b, hi = (int)(uint32_t)(b >> 32);
+  const uint32_t l = (uint32_t)__builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xF, 0xF, false);
+  const uint32_t h = (uint32_t)__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, ((uint64_t)h << 32) | l);
+}
+// row_ror:n rotates inside each row of 16 lanes
+constexpr int kRor8 = 0x128, kRor4 = 0x124, kRor2 = 0x122, kRor1 = 0x121;
+__device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, kRor8, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, kRor4, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, kRor2, 0xF, 0xF, false));
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, kRor1, 0xF, 0xF, false));
+}
+
+// ---------------------------------------------------------------- 16/32-bit elements
+template <int DT> struct Elem;
+template <> struct Elem<GPTQ_F32> {
+  typedef float type;
+  static __device__ __forceinline__ float up(float x) { return x; }
+  static __device__ __forceinline__ float down(float x) { return x; }
+};
+template <> struct Elem<GPTQ_BF16> {
+  typedef __bf16 type;
+  static __device__ __forceinline__ float up(__bf16 x) { return (float)x; }
+  static __device__ __forceinline__ __bf16 down(float x) { return (__bf16)x; }
+};
+template <> struct Elem<GPTQ_F16> {
+  typedef _Float16 type;
+  static __device__ __forceinline__ float up(_Float16 x) { return (float)x; }
+  static __device__ __forceinline__ _Float16 down(float x) { return (_Float16)x; }
+};
+
+// Eight consecutive elements, `n` of them present (the others are zero).
+// Full pieces are copied whole at whatever alignment the caller's rows have:
+// gfx950 loads and stores wide words at any byte address in global memory.
+template <int DT>
+__device__ __forceinline__ void load8(const typename Elem<DT>::type* p, int n, float (&v)[8]) {
+  typedef typename Elem<DT>::type T;
+  T x[8];
+  if (n >= 8) {
+    __builtin_memcpy(x, p, sizeof x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = Elem<DT>::up(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem<DT>::up(p[i]) : 0.f;
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store8(typename Elem<DT>::type* p, int n, const float (&v)[8]) {
+  typedef typename Elem<DT>::type T;
+  T x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = Elem<DT>::down(v[i]);
+  if (n >= 8) {
+    __builtin_memcpy(p, x, sizeof x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = x[i];
+  }
+}
+__device__ __forceinline__ void store_codes8(uint8_t* p, int n, uint32_t lo, uint32_t hi) {
+  if (n >= 8) {
+    const uint32_t x[2] = {lo, hi};
+    __builtin_memcpy(p, x, 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+  }
+}
+
+}  // namespace gq

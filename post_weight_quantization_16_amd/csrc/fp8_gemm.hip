@@ -1,0 +1,635 @@
+// Products of block-scaled e4m3 matrices (fp8.hpp has the format):
+//   C[m,n] = Σ_kb sa[m,kb]·sb[n/128,kb]·Σ_{k in kb} a[m,k]·b[n,k]
+// and the gated projection act(A·Gᵀ)·(A·Uᵀ), rounded to 16 or 32 bits or
+// quantized again in 1 x 128 blocks.
+//
+// A block of 128 along K is contracted on the matrix cores from a zero
+// accumulator and comes in with one fma a value: acc += t·(sa·sb).  The
+// weights are the instruction's first operand: a lane then holds one row m of
+// C (its lane % 16) and four neighbouring columns n (4·(lane / 16) + 0..3), so
+// sa is one register and four outputs are stored together.  Any order of k
+// inside a block gives the same sum if both operands agree on it: lane l
+// takes bytes 16·(l / 16).. and 64 + 16·(l / 16).. of its row's block.
+//
+// Two ways to contract a block:
+//   fast   one v_mfma_f32_16x16x128_f8f6f4.  It aligns each eight products
+//          to the largest of them and drops what lies more than 2^13 below:
+//          measured 1.4e-5 of the result's norm on normal data and up to
+//          9e-5 of Σ|a||b| with outlier columns.  Taken where C has 16 bits,
+//          whose own rounding (2^-11, 2^-8) is larger.
+//   exact  e4m3 -> fp16 (every value is exact) in registers and four
+//          v_mfma_f32_16x16x32_f16: products exact, sums in fp32 (measured
+//          below 5·2^-24 of Σ|a||b| a block), at half the rate.  Taken for
+//          fp32 results and for 8-bit ones, whose scales are fp32.
+#include "fp8.hpp"
+
+namespace gq {
+namespace {
+
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+typedef __attribute__((ext_vector_type(4))) int i32x4;
+
+struct GArgs {
+  const uint8_t* A; const float* sa; int64_t M, K, lda;
+  const uint8_t* B[2]; const float* sb[2]; int64_t N, ldb[2];   // gate and up, or B alone
+  void* C; int64_t ldc; int c_dt, act;
+  uint8_t* codes; int64_t ld_codes; float* sc; int64_t nb;      // nb = blocks of N
+  float* P;          // split-K partials [splits][1 or 2][M][N]
+  int kb, kper;      // blocks of K, and of one split
+  int tm, tn;        // tiles
+  int wide;          // every row of A and B starts at a multiple of 16 bytes
+};
+
+// ---------------------------------------------------------------- a block's contraction
+// 128 bytes of a row, this lane's 32 of them.
+template <bool FAST> struct Frag;
+template <> struct Frag<true> {
+  i32x8 v;
+  __device__ __forceinline__ void set(const i32x4& x, const i32x4& y) {
+    v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+template <> struct Frag<false> {
+  f16x8 v[4];
+  static __device__ __forceinline__ f16x8 up(int lo, int hi) {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false);
+    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
+    return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
+  __device__ __forceinline__ void set(const i32x4& x, const i32x4& y) {
+    v[0] = up(x[0], x[1]); v[1] = up(x[2], x[3]);
+    v[2] = up(y[0], y[1]); v[3] = up(y[2], y[3]);
+  }
+};
+__device__ __forceinline__ f32x4 contract(const Frag<true>& b, const Frag<true>& a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,
+                                                          0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 contract(const Frag<false>& b, const Frag<false>& a) {
+  f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[i], a.v[i], t, 0, 0, 0);
+  return t;
+}
+
+// 16 bytes of a row from byte k on; bytes past the row's K and rows that do
+// not exist are zero.
+__device__ __forceinline__ i32x4 piece16(const uint8_t* row, int64_t k, int64_t K, bool ok) {
+  i32x4 v = {0, 0, 0, 0};
+  if (ok && k + 16 <= K) {
+    __builtin_memcpy(&v, row + k, 16);
+  } else if (ok) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (k + i < K) v[i >> 2] |= (int)((uint32_t)row[k + i] << (8 * (i & 3)));
+  }
+  return v;
+}
+
+// ---------------------------------------------------------------- epilogues
+__device__ __forceinline__ float activate(float x, int act) {
+  if (act == GPTQ_ACT_SILU) return x / (1.f + expf(-x));
+  if (act == GPTQ_ACT_GELU) return 0.5f * x * erfcf(x * -0.70710678f);   // Φ(x) without cancellation
+  return x / (1.f + expf(-1.5957691f * (x + 0.044715f * x * x * x)));    // (1 + tanh z)/2 = 1/(1 + e^-2z)
+}
+
+// Four neighbouring values of a row, `n` of them present.
+template <int DT> __device__ __forceinline__ void put4(void* C, int64_t at, int n, const f32x4& x) {
+  typedef typename Elem<DT>::type T;
+  T v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = Elem<DT>::down(x[i]);
+  T* p = static_cast<T*>(C) + at;
+  if (n >= 4) {
+    __builtin_memcpy(p, v, sizeof v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void put4_dt(void* C, int dt, int64_t at, int n, const f32x4& x) {
+  if (dt == GPTQ_F32) put4<GPTQ_F32>(C, at, n, x);
+  else if (dt == GPTQ_BF16) put4<GPTQ_BF16>(C, at, n, x);
+  else put4<GPTQ_F16>(C, at, n, x);
+}
+
+// Magnitudes as integers: finite < infinity < NaN.
+__device__ __forceinline__ uint32_t mag_bits(float x) {
+  return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
+}
+
+// ---------------------------------------------------------------- tile kernel
+// BM x BN tile of C per workgroup, waves of WM x WN, K in stages of one block
+// in a ring of NS stage buffers.  Stages go from memory straight into LDS
+// (global_load_lds: no registers, no LDS store instructions), NS-1 ahead;
+// a wave waits for its own copies of the next stage, then one barrier
+// publishes everyone's and frees the buffer just read.
+// LDS per stage: BM + BN rows of 128 bytes (16-byte piece p of row r in slot
+// p ^ ((r >> 1) & 7): the 16 rows that a lane group reads together cover all
+// 64 banks), then BM scales of A.
+// GATED: the B rows are BN/2 gate rows, then BN/2 up rows of the same
+// columns, and a wave's columns are half gate, half up.
+template <int BM, int BN, int WM, int WN, int NS> struct Tile {
+  static constexpr int WAVES = (BM / WM) * (BN / WN), NT = WAVES * 64;
+  static constexpr int MI = WM / 16, NI = WN / 16;
+  static constexpr int SEGS = (BM + BN) / 8;            // 1-KB copies per stage
+  static constexpr int PER = SEGS / WAVES;              // ... per wave
+  static constexpr int NW = PER + 1;                    // with one of 64 scales
+  static constexpr int SB = (BM + BN) * 128 + BM * 4;   // bytes per stage
+  static constexpr int SMEM = NS * SB;
+  static_assert(SEGS % WAVES == 0 && WAVES >= BM / 64 && NS >= 2, "copy plan");
+  static_assert((NS - 2) * NW <= 63, "vmcnt range");
+};
+
+constexpr int wait_imm(int n) { return ((n >> 4) << 14) | (n & 15) | 0x70; }   // vmcnt(n), lgkmcnt(0)
+template <int NW> __device__ __forceinline__ void wait_copies(int ahead) {
+  if (ahead <= 0) __builtin_amdgcn_s_waitcnt(wait_imm(0));
+  else if (ahead == 1) __builtin_amdgcn_s_waitcnt(wait_imm(NW));
+  else __builtin_amdgcn_s_waitcnt(wait_imm(2 * NW));
+}
+
+// Tile of a workgroup.  Workgroup L runs on XCD L % 8: each XCD takes one
+// stretch of the tile order, which goes down strips of eight tile rows, so
+// the tiles an XCD's L2 serves at a time share rows of A and of B.
+__device__ __forceinline__ void tile_of(uint32_t L, uint32_t total, uint32_t tm, uint32_t tn,
+                                        uint32_t& bm, uint32_t& bn) {
+  const uint32_t q = total / 8, r = total % 8, x = L % 8;
+  const uint32_t u = x * q + min(x, r) + L / 8;
+  const uint32_t strip = u / (8 * tn), rows = min(8u, tm - strip * 8), in = u - strip * 8 * tn;
+  bm = strip * 8 + in % rows;
+  bn = in / rows;
+}
+
+enum { kStore = 0, kPartial = 1, kCodes = 2 };
+
+template <int BM, int BN, int WM, int WN, int NS, bool FAST, bool GATED, int EPI>
+__global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel(GArgs a) {
+  using T = Tile<BM, BN, WM, WN, NS>;
+  constexpr int MI = T::MI, NI = T::NI, NB = GATED ? 2 : 1;
+  constexpr int BC = BN / NB;      // columns of C
+  constexpr int WC = WN / NB;      // ... of a wave
+  __shared__ __attribute__((aligned(1024))) char S[T::SMEM];
+  const int t = threadIdx.x, lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = w / (BN / WN), wn = w % (BN / WN);
+  uint32_t bm, bn;
+  const uint32_t tiles = (uint32_t)a.tm * a.tn, split = blockIdx.x / tiles;
+  tile_of(blockIdx.x - split * tiles, tiles, a.tm, a.tn, bm, bn);
+  const int64_t m0 = (int64_t)bm * BM, n0 = (int64_t)bn * BC;
+  const int kbeg = (int)split * a.kper, kend = min(a.kb, kbeg + a.kper);
+  const int nst = kend - kbeg;
+
+  // copy plan: wave w's copy i fills KB w·PER + i of the stage: rows 8·seg..,
+  // lane l row l/8 of them, slot l%8
+  const uint8_t* src[T::PER];
+#pragma unroll
+  for (int i = 0; i < T::PER; ++i) {
+    const int row = (w * T::PER + i) * 8 + (lane >> 3);
+    const int p = (lane & 7) ^ ((row >> 1) & 7);
+    const uint8_t* base;
+    if (row < BM) {
+      base = a.A + min(m0 + row, a.M - 1) * a.lda;
+    } else {
+      const int br = row - BM, half = GATED ? br / BC : 0;
+      base = a.B[half] + min(n0 + (br - half * BC), a.N - 1) * a.ldb[half];
+    }
+    src[i] = base + (int64_t)kbeg * 128 + p * 16;
+  }
+  const int srow = (w % (BM / 64)) * 64 + lane;
+  const float* ssrc = a.sa + min(m0 + srow, a.M - 1) * a.kb + kbeg;
+  const unsigned sbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)S;
+  const bool ragged = (a.K & 127) != 0;
+  auto copy = [&](int st) {
+    const unsigned lb = sbase + (unsigned)((st % NS) * T::SB);
+    if (a.wide && !(ragged && kbeg + st == a.kb - 1)) {
+#pragma unroll
+      for (int i = 0; i < T::PER; ++i)
+        // 16 bytes per lane from the address to LDS M0 + 16·lane; no register
+        // result, ordered before the reads by the stage waits
+        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+                     :: "s"(lb + (unsigned)(w * T::PER + i) * 1024u), "v"(src[i] + (int64_t)st * 128)
+                     : "memory");
+      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
+                   :: "s"(lb + (unsigned)((BM + BN) * 128 + (w % (BM / 64)) * 256)), "v"(ssrc + st)
+                   : "memory");
+    } else {
+      // rows that end inside this block, or that start at odd addresses
+      char* b = S + (st % NS) * T::SB;
+      for (int i = 0; i < T::PER; ++i) {
+        const int seg = w * T::PER + i, row = seg * 8 + (lane >> 3);
+        const int p = (lane & 7) ^ ((row >> 1) & 7);
+        const int64_t k = (int64_t)(kbeg + st) * 128 + p * 16;
+        const i32x4 v = piece16(src[i] + (int64_t)st * 128 - k, k, a.K, true);
+        *reinterpret_cast<i32x4*>(b + seg * 1024 + lane * 16) = v;
+      }
+      *reinterpret_cast<float*>(b + (BM + BN) * 128 + srow * 4) = ssrc[st];
+      __builtin_amdgcn_s_waitcnt(wait_imm(0));
+    }
+  };
+
+  f32x4 acc[NI][MI];
+#pragma unroll
+  for (int j = 0; j < NI; ++j)
+#pragma unroll
+    for (int i = 0; i < MI; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const float* sbp[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int64_t blk = min((n0 + wn * WC) / 128, a.nb - 1);
+    sbp[b] = a.sb[b] + blk * a.kb + kbeg;
+  }
+  const int l15 = lane & 15, sw = ((lane >> 4) ^ ((l15 >> 1) & 7)) << 4;
+  const int arow = (wm * WM + l15) * 128 + sw;
+  int brow[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) brow[b] = (BM + b * BC + wn * WC + l15) * 128 + sw;
+  const int soff = (BM + BN) * 128 + (wm * WM + l15) * 4;
+
+  for (int s0 = 0; s0 < NS - 1 && s0 < nst; ++s0) copy(s0);
+  wait_copies<T::NW>(min(nst - 1, NS - 2));
+  __syncthreads();
+  for (int st = 0; st < nst; ++st) {
+    if (st + NS - 1 < nst) copy(st + NS - 1);
+    const char* b = S + (st % NS) * T::SB;
+    float sb[NB];
+#pragma unroll
+    for (int q = 0; q < NB; ++q) sb[q] = sbp[q][st];
+    Frag<FAST> fb[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int off = brow[GATED ? j / (NI / 2) : 0] + (GATED ? j % (NI / 2) : j) * 2048;
+      fb[j].set(*reinterpret_cast<const i32x4*>(b + off), *reinterpret_cast<const i32x4*>(b + (off ^ 64)));
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      Frag<FAST> fa;
+      const int off = arow + i * 2048;
+      fa.set(*reinterpret_cast<const i32x4*>(b + off), *reinterpret_cast<const i32x4*>(b + (off ^ 64)));
+      const float sa = *reinterpret_cast<const float*>(b + soff + i * 64);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const f32x4 p = contract(fb[j], fa);
+        const float s = sa * sb[GATED ? j / (NI / 2) : 0];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][i][r] = __builtin_fmaf(p[r], s, acc[j][i][r]);
+      }
+    }
+    wait_copies<T::NW>(min(nst - 1, st + NS - 1) - (st + 1));
+    __syncthreads();
+  }
+
+  if constexpr (EPI == kPartial) {
+    float* P = a.P + (int64_t)split * NB * a.M * a.N;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int64_t m = m0 + wm * WM + i * 16 + l15;
+      if (m >= a.M) continue;
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const int half = GATED ? j / (NI / 2) : 0;
+        const int64_t n = n0 + wn * WC + (GATED ? j % (NI / 2) : j) * 16 + 4 * (lane >> 4);
+        if (n < a.N)
+          put4<GPTQ_F32>(P, ((int64_t)half * a.M + m) * a.N + n, (int)min((int64_t)4, a.N - n), acc[j][i]);
+      }
+    }
+    return;
+  }
+  constexpr int NO = GATED ? NI / 2 : NI;   // 16-column pieces of C
+  if constexpr (GATED) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NO; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][i][r] = activate(acc[j][i][r], a.act) * acc[NO + j][i][r];
+  }
+  if constexpr (EPI == kStore) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int64_t m = m0 + wm * WM + i * 16 + l15;
+      if (m >= a.M) continue;
+#pragma unroll
+      for (int j = 0; j < NO; ++j) {
+        const int64_t n = n0 + wn * WC + j * 16 + 4 * (lane >> 4);
+        if (n < a.N) put4_dt(a.C, a.c_dt, m * a.ldc + n, (int)min((int64_t)4, a.N - n), acc[j][i]);
+      }
+    }
+  } else {
+    // the tile's 128 columns are one block of its rows
+    static_assert(EPI != kCodes || BC == 128, "a tile is one block wide");
+    uint32_t* top = reinterpret_cast<uint32_t*>(S);   // [BN / WN][BM]
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      uint32_t u = 0;
+#pragma unroll
+      for (int j = 0; j < NO; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int64_t n = n0 + wn * WC + j * 16 + 4 * (lane >> 4) + r;
+          if (n < a.N) u = max(u, mag_bits(acc[j][i][r]));
+        }
+      u = max(u, (uint32_t)__shfl_xor((int)u, 16));
+      u = max(u, (uint32_t)__shfl_xor((int)u, 32));
+      if (lane < 16) top[wn * BM + wm * WM + i * 16 + l15] = u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int64_t m = m0 + wm * WM + i * 16 + l15;
+      uint32_t u = 0;
+#pragma unroll
+      for (int q = 0; q < BN / WN; ++q) u = max(u, top[q * BM + wm * WM + i * 16 + l15]);
+      const float s = e4m3_scale((double)__builtin_bit_cast(float, u));
+      const double sd = (double)s, inv = 1.0 / sd;
+      if (m >= a.M) continue;
+      if (wn == 0 && lane < 16) a.sc[m * a.nb + bn] = s;
+#pragma unroll
+      for (int j = 0; j < NO; ++j) {
+        const int64_t n = n0 + wn * WC + j * 16 + 4 * (lane >> 4);
+        float q[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) q[r] = e4m3_quotient((double)acc[j][i][r], sd, inv);
+        const uint32_t c = e4m3_pack4(q[0], q[1], q[2], q[3]);
+        uint8_t* p = a.codes + m * a.ld_codes + n;
+        if (n + 4 <= a.N) {
+          __builtin_memcpy(p, &c, 4);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (n + r < a.N) p[r] = (uint8_t)(c >> (8 * r));
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+// Up to 16 rows of A: the weights' bytes are what counts.  A workgroup owns
+// 16 columns (of gate and up for GATED) and its eight waves every eighth
+// block of K; operands go from memory straight into registers, each weight
+// byte once, D blocks in flight; the waves' sums are added in wave order.
+constexpr int kFewRows = 16, kFewWaves = 8;
+
+template <bool FAST, bool GATED, int EPI>
+__global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GArgs a) {
+  constexpr int NB = GATED ? 2 : 1, D = GATED ? 2 : 4;
+  __shared__ float part[kFewWaves][NB][16][17];
+  const int t = threadIdx.x, lane = t & 63, l15 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const bool mok = l15 < a.M, nok = n0 + l15 < a.N;
+  const int64_t blk = n0 / 128;
+  const int kp = 16 * (lane >> 4);
+  const uint8_t* ap = a.A + (mok ? l15 : 0) * a.lda;
+  const uint8_t* bp[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) bp[b] = a.B[b] + (nok ? n0 + l15 : a.N - 1) * a.ldb[b];
+  const float* sap = a.sa + (mok ? l15 : 0) * (int64_t)a.kb;
+  f32x4 acc[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  i32x4 ra[D][2], rb[D][NB][2];
+  float s[D][NB];
+  const int full = (int)(a.K / 128);   // whole blocks
+  auto load = [&](int d, int kb) {
+    if (kb < full) {
+      const int64_t k = (int64_t)kb * 128 + kp;
+      __builtin_memcpy(&ra[d][0], ap + k, 16);
+      __builtin_memcpy(&ra[d][1], ap + k + 64, 16);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        __builtin_memcpy(&rb[d][b][0], bp[b] + k, 16);
+        __builtin_memcpy(&rb[d][b][1], bp[b] + k + 64, 16);
+      }
+    } else if (kb < a.kb) {
+      const int64_t k = (int64_t)kb * 128 + kp;
+      ra[d][0] = piece16(ap, k, a.K, true);
+      ra[d][1] = piece16(ap, k + 64, a.K, true);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        rb[d][b][0] = piece16(bp[b], k, a.K, true);
+        rb[d][b][1] = piece16(bp[b], k + 64, a.K, true);
+      }
+    }
+    if (kb < a.kb) {
+      const float x = sap[kb];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) s[d][b] = x * a.sb[b][blk * a.kb + kb];
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, w + d * kFewWaves);
+  for (int k0 = w; k0 < a.kb; k0 += D * kFewWaves) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int kb = k0 + d * kFewWaves;
+      if (kb >= a.kb) break;
+      Frag<FAST> fa;
+      fa.set(ra[d][0], ra[d][1]);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        Frag<FAST> fb;
+        fb.set(rb[d][b][0], rb[d][b][1]);
+        const f32x4 p = contract(fb, fa);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[b][r] = __builtin_fmaf(p[r], s[d][b], acc[b][r]);
+      }
+      load(d, kb + D * kFewWaves);
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) part[w][b][l15][4 * (lane >> 4) + r] = acc[b][r];
+  __syncthreads();
+  if (t >= 256) return;
+  const int m = t >> 4, c = t & 15;
+  const int64_t n = n0 + c;
+  if (m >= a.M || n >= a.N) return;
+  float h[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    h[b] = 0.f;
+#pragma unroll
+    for (int q = 0; q < kFewWaves; ++q) h[b] += part[q][b][m][c];
+  }
+  float x = h[0];
+  if constexpr (GATED) x = activate(h[0], a.act) * h[NB - 1];
+  if constexpr (EPI == kPartial) {
+    a.P[(int64_t)m * a.N + n] = x;     // h itself: one partial, activated
+  } else {
+    if (a.c_dt == GPTQ_F32) static_cast<float*>(a.C)[m * a.ldc + n] = x;
+    else if (a.c_dt == GPTQ_BF16) static_cast<__bf16*>(a.C)[m * a.ldc + n] = (__bf16)x;
+    else static_cast<_Float16*>(a.C)[m * a.ldc + n] = (_Float16)x;
+  }
+}
+
+// ---------------------------------------------------------------- joining partial sums
+// One thread per eight columns: the partials in split order, then the
+// activation (gated, not yet activated) and C, or a block's codes and scale
+// (16 lanes a block).
+template <bool GATED, bool CODES>
+__global__ __launch_bounds__(256) void join_kernel(GArgs a, int splits) {
+  constexpr int NB = GATED ? 2 : 1;
+  const int t = threadIdx.x, lane = t & 15;
+  const int64_t g = (int64_t)blockIdx.x * 16 + (t >> 4);
+  const int64_t m = g / a.nb, blk = g - m * a.nb;
+  if (m >= a.M) return;
+  const int64_t n = blk * 128 + lane * 8;
+  const int c = (int)max((int64_t)0, min((int64_t)8, a.N - n));
+  float h[NB][8];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[b][i] = 0.f;
+    for (int s = 0; s < splits; ++s) {
+      float v[8];
+      load8<GPTQ_F32>(a.P + (((int64_t)s * NB + b) * a.M + m) * a.N + n, c, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[b][i] += v[i];
+    }
+  }
+  if constexpr (GATED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[0][i] = activate(h[0][i], a.act) * h[NB - 1][i];
+  }
+  if constexpr (CODES) {
+    uint32_t u = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u = max(u, mag_bits(h[0][i]));
+    const float s = e4m3_scale((double)__builtin_bit_cast(float, row16_max_u32(u)));
+    const double sd = (double)s, inv = 1.0 / sd;
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = e4m3_quotient((double)h[0][i], sd, inv);
+    store_codes8(a.codes + m * a.ld_codes + n, c, e4m3_pack4(q[0], q[1], q[2], q[3]),
+                 e4m3_pack4(q[4], q[5], q[6], q[7]));
+    if (lane == 0) a.sc[m * a.nb + blk] = s;
+  } else {
+    if (a.c_dt == GPTQ_F32) store8<GPTQ_F32>(static_cast<float*>(a.C) + m * a.ldc + n, c, h[0]);
+    else if (a.c_dt == GPTQ_BF16) store8<GPTQ_BF16>(static_cast<__bf16*>(a.C) + m * a.ldc + n, c, h[0]);
+    else store8<GPTQ_F16>(static_cast<_Float16*>(a.C) + m * a.ldc + n, c, h[0]);
+  }
+}
+
+// ---------------------------------------------------------------- choice and launch
+struct Plan { int bm, bc; int splits, kper; bool few; };
+
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool ws) {
+  Plan p{};
+  const int kb = (int)ceil_div(K, 128);
+  p.few = M <= kFewRows;
+  p.splits = 1;
+  p.kper = kb;
+  if (p.few) return p;
+  const int64_t big = ceil_div(M, 256) * ceil_div(N, gated ? 128 : 256);
+  const bool large = big >= 192;
+  p.bm = large ? 256 : 128;
+  p.bc = large ? (gated ? 128 : 256) : 128;
+  if (ws && !large) {
+    const int64_t tiles = ceil_div(M, p.bm) * ceil_div(N, p.bc);
+    const int64_t s = std::min<int64_t>(std::min<int64_t>(ceil_div(256, tiles), 16), kb / 2);
+    if (s > 1) {
+      p.kper = (int)ceil_div(kb, s);
+      p.splits = (int)ceil_div(kb, p.kper);
+    }
+  }
+  return p;
+}
+
+template <int BM, int BN, int WM, int WN, int NS, bool FAST, bool GATED, int EPI>
+hipError_t launch_tile(GArgs& a, int splits, hipStream_t s) {
+  using T = Tile<BM, BN, WM, WN, NS>;
+  a.tm = (int)ceil_div(a.M, BM);
+  a.tn = (int)ceil_div(a.N, GATED ? BN / 2 : BN);
+  const int64_t grid = (int64_t)a.tm * a.tn * splits;
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  tile_kernel<BM, BN, WM, WN, NS, FAST, GATED, EPI><<<(unsigned)grid, T::NT, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <bool GATED, bool FAST>
+hipError_t run(GArgs& a, void* ws, hipStream_t s) {
+  const Plan p = plan_of(a.M, a.N, a.K, GATED, ws != nullptr);
+  a.nb = ceil_div(a.N, 128);
+  a.kb = (int)ceil_div(a.K, 128);
+  a.kper = p.kper;
+  a.P = static_cast<float*>(ws);
+  a.wide = (uintptr_t)a.A % 16 == 0 && (a.M == 1 || a.lda % 16 == 0);
+  for (int b = 0; b < (GATED ? 2 : 1); ++b)
+    a.wide = a.wide && (uintptr_t)a.B[b] % 16 == 0 && (a.N == 1 || a.ldb[b] % 16 == 0);
+  const bool codes = GATED && a.codes;
+  hipError_t e;
+  if (p.few && !(codes && !ws)) {
+    const unsigned grid = (unsigned)ceil_div(a.N, 16);
+    if (!codes) {
+      few_rows_kernel<FAST, GATED, kStore><<<grid, kFewWaves * 64, 0, s>>>(a);
+      return hipGetLastError();
+    }
+    few_rows_kernel<FAST, GATED, kPartial><<<grid, kFewWaves * 64, 0, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    join_kernel<false, true><<<(unsigned)ceil_div(a.M * a.nb, 16), 256, 0, s>>>(a, 1);
+    return hipGetLastError();
+  }
+  if (p.splits > 1) {
+    e = GATED ? launch_tile<128, 256, 64, 64, 2, FAST, GATED, kPartial>(a, p.splits, s)
+              : launch_tile<128, 128, 64, 64, 2, FAST, GATED, kPartial>(a, p.splits, s);
+    if (e != hipSuccess) return e;
+    const int64_t grid = ceil_div(a.M * a.nb, 16);
+    if (codes) join_kernel<GATED, true><<<(unsigned)grid, 256, 0, s>>>(a, p.splits);
+    else join_kernel<GATED, false><<<(unsigned)grid, 256, 0, s>>>(a, p.splits);
+    return hipGetLastError();
+  }
+  if constexpr (GATED) {
+    if (p.bm == 256)
+      return codes ? launch_tile<256, 256, 128, 64, 2, FAST, true, kCodes>(a, 1, s)
+                   : launch_tile<256, 256, 128, 64, 2, FAST, true, kStore>(a, 1, s);
+    return codes ? launch_tile<128, 256, 64, 64, 2, FAST, true, kCodes>(a, 1, s)
+                 : launch_tile<128, 256, 64, 64, 2, FAST, true, kStore>(a, 1, s);
+  } else {
+    return p.bm == 256 ? launch_tile<256, 256, 128, 64, 2, FAST, false, kStore>(a, 1, s)
+                       : launch_tile<128, 128, 64, 64, 2, FAST, false, kStore>(a, 1, s);
+  }
+}
+
+size_t ws_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
+  const Plan p = plan_of(M, N, K, gated, true);
+  if (p.few) return gated ? align_up((size_t)M * N * 4) : 256;
+  return p.splits > 1 ? align_up((size_t)p.splits * (gated ? 2 : 1) * M * N * 4) : 256;
+}
+
+}  // namespace
+
+size_t fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K) { return ws_bytes(M, N, K, false); }
+size_t fp8_gated_ws_bytes(int64_t M, int64_t N, int64_t K) { return ws_bytes(M, N, K, true); }
+
+hipError_t fp8_gemm_launch(const uint8_t* A, const float* sa, int64_t M, int64_t K, int64_t lda,
+                           const uint8_t* B, const float* sb, int64_t N, int64_t ldb, void* C,
+                           int c_dt, int64_t ldc, void* ws, hipStream_t s) {
+  GArgs a{};
+  a.A = A; a.sa = sa; a.M = M; a.K = K; a.lda = lda;
+  a.B[0] = B; a.sb[0] = sb; a.N = N; a.ldb[0] = ldb;
+  a.C = C; a.ldc = ldc; a.c_dt = c_dt;
+  return c_dt == GPTQ_F32 ? run<false, false>(a, ws, s) : run<false, true>(a, ws, s);
+}
+
+hipError_t fp8_gated_launch(const uint8_t* A, const float* sa, int64_t M, int64_t K, int64_t lda,
+                            const uint8_t* G, const float* sg, int64_t ldg, const uint8_t* U,
+                            const float* su, int64_t ldu, int64_t N, int act, void* C, int c_dt,
+                            int64_t ldc, uint8_t* codes, int64_t ld_codes, float* sc, void* ws,
+                            hipStream_t s) {
+  GArgs a{};
+  a.A = A; a.sa = sa; a.M = M; a.K = K; a.lda = lda;
+  a.B[0] = G; a.sb[0] = sg; a.ldb[0] = ldg;
+  a.B[1] = U; a.sb[1] = su; a.ldb[1] = ldu; a.N = N;
+  a.C = C; a.ldc = ldc; a.c_dt = c_dt; a.act = act;
+  a.codes = codes; a.ld_codes = ld_codes; a.sc = sc;
+  return codes || c_dt == GPTQ_F32 ? run<true, false>(a, ws, s) : run<true, true>(a, ws, s);
+}
+
+}  // namespace gq

@@ -1,0 +1,172 @@
+"""The 8-bit floating-point calls without a GPU: pins of the oracle, and every
+argument check of the C ABI and of the binding."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import post_weight_quantization_16_amd as g
+from oracle import fp8
+from post_weight_quantization_16_amd import _native as n
+
+FAKE = 1 << 20   # never dereferenced: every call below returns before any HIP call
+E4 = torch.float8_e4m3fn
+
+
+# ---------------------------------------------------------------- oracle
+def test_grid_is_the_format():
+    codes = torch.arange(256, dtype=torch.uint8)
+    want = codes.view(E4).double().numpy()
+    got = fp8.decode(codes.numpy())
+    assert np.array_equal(got, want, equal_nan=True)
+    assert fp8.GRID[-1] == 448
+
+
+def test_nearest_rounds_like_the_format():
+    """Against torch's conversion from values that fp32 holds exactly: every
+    code, every border and its fp32 neighbours."""
+    v = np.concatenate([fp8.GRID, fp8._MID, fp8._MID * (1 + 2.0 ** -20), fp8._MID * (1 - 2.0 ** -20)])
+    v = np.concatenate([v, -v]).astype(np.float32)
+    want = torch.from_numpy(v).to(E4).double().numpy()
+    assert np.array_equal(fp8.nearest(v.astype(np.float64)), want)
+
+
+def test_quantize_closed_forms():
+    x = np.zeros((3, 300))
+    x[1, 0], x[1, 130], x[2, 5] = 448.0, -7.0, np.inf
+    v, s = fp8.quantize(x, 1)
+    assert s[0, 0] == np.float32(2.0 ** -126) and s[1, 0] == 1 and s[1, 1] == np.float32(7 / 448)
+    assert v[1, 0] == 448 and v[1, 130] == -448 and np.all(v[0] == 0)
+    assert np.isnan(s[2, 0]) and np.all(np.isnan(v[2, :128])) and np.all(v[2, 128:] == 0)
+    v, s = fp8.quantize(x[:2], 128)
+    assert s.shape == (1, 3) and s[0, 0] == 1 and v[1, 130] == -448
+
+
+def test_products_of_blocks():
+    rng = np.random.default_rng(0)
+    a = fp8.quantize(rng.standard_normal((3, 200)), 1)
+    b = fp8.quantize(rng.standard_normal((130, 200)), 128)
+    c, mag = fp8.matmul(a, b)
+    want = sum(a[0][1, k] * float(a[1][1, k // 128]) * b[0][129, k] * float(b[1][1, k // 128]) for k in range(200))
+    assert abs(c[1, 129] - want) < 1e-12 and np.all(mag >= np.abs(c))
+    assert fp8.activation(np.array([0.0, 30.0]), "silu").tolist() == [0.0, 30.0 / (1 + np.exp(-30.0))]
+    x = np.linspace(-4, 4, 9)
+    assert np.allclose(fp8.activation(x, "gelu_tanh"),
+                       0.5 * x * (1 + np.tanh(np.sqrt(2 / np.pi) * (x + 0.044715 * x ** 3))), rtol=1e-12)
+
+
+# ---------------------------------------------------------------- C ABI
+def test_quantize_refusals():
+    f = n.lib().gptq_fp8_quantize
+    call = lambda X=FAKE, dt=n.BF16, rows=4, cols=200, ld=200, br=1, c=FAKE, ldc=200, s=FAKE: f(
+        X, dt, rows, cols, ld, br, c, ldc, s, None)
+    for kw in [dict(X=None), dict(c=None), dict(s=None), dict(dt=7), dict(rows=-1), dict(cols=0),
+               dict(cols=65537, ld=65537, ldc=65537), dict(ld=199), dict(ldc=199), dict(br=2), dict(br=0),
+               dict(X=FAKE + 1), dict(X=FAKE + 2, dt=n.F32), dict(s=FAKE + 2), dict(rows=(1 << 24) + 1)]:
+        assert call(**kw) == n.ERR_INVALID_ARG, kw
+        assert n.last_error()
+    assert call(X=None, c=None, s=None, rows=0) == n.OK
+
+
+def test_rmsnorm_refusals():
+    f = n.lib().gptq_rmsnorm_fp8
+
+    def call(X=FAKE, ldx=200, R=None, ldr=0, dt=n.BF16, gm=FAKE, gdt=n.BF16, rows=4, cols=200, eps=1e-5,
+             H=None, ldh=0, Y=None, ldy=0, c=FAKE, ldc=200, s=FAKE):
+        return f(X, ldx, R, ldr, dt, gm, gdt, rows, cols, eps, H, ldh, Y, ldy, c, ldc, s, None)
+
+    other = FAKE + (1 << 16)
+    for kw in [dict(X=None), dict(gm=None), dict(dt=9), dict(gdt=n.F16), dict(rows=-1), dict(cols=0),
+               dict(ldx=199), dict(R=other, ldr=100), dict(H=other, ldh=100), dict(Y=other, ldy=100), dict(ldc=100),
+               dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(c=None), dict(s=None),
+               dict(c=None, s=None), dict(H=FAKE, ldh=300), dict(R=other, ldr=200, H=other, ldh=201),
+               dict(Y=FAKE, ldy=200), dict(Y=other, ldy=200, R=other, ldr=200), dict(Y=other, ldy=200, H=other, ldh=200),
+               dict(X=FAKE + 1), dict(gm=FAKE + 2, gdt=n.F32), dict(s=FAKE + 1), dict(Y=other + 1, ldy=200)]:
+        assert call(**kw) == n.ERR_INVALID_ARG, kw
+    assert call(X=None, gm=None, c=None, s=None, rows=0) == n.OK
+
+
+def test_gemm_refusals():
+    f = n.lib().gptq_fp8_gemm
+
+    def call(A=FAKE, sa=FAKE, M=4, K=256, lda=256, B=FAKE, sb=FAKE, N=64, ldb=256, C=FAKE, dt=n.BF16, ldc=64,
+             ws=None, wsb=0):
+        return f(A, sa, M, K, lda, B, sb, N, ldb, C, dt, ldc, ws, wsb, None)
+
+    for kw in [dict(A=None), dict(sa=None), dict(B=None), dict(sb=None), dict(C=None), dict(M=-1), dict(K=0), dict(N=0),
+               dict(K=70000, lda=70000, ldb=70000), dict(lda=255), dict(ldb=255), dict(ldc=63), dict(dt=5),
+               dict(sa=FAKE + 2), dict(C=FAKE + 1), dict(C=FAKE + 2, dt=n.F32)]:
+        assert call(**kw) == n.ERR_INVALID_ARG, kw
+    ws = n.lib().gptq_workspace_bytes
+    need = ws(n.WS_FP8_GEMM, 64, 256, 4, None)
+    assert need > 0 and need % 256 == 0
+    assert call(ws=FAKE, wsb=need - 1) == n.ERR_WORKSPACE
+    assert call(ws=FAKE + 8, wsb=need) == n.ERR_WORKSPACE
+    assert call(A=None, sa=None, C=None, M=0) == n.OK
+    for which in (n.WS_FP8_GEMM, n.WS_FP8_GATED):
+        assert ws(which, 0, 256, 4, None) == 0 and ws(which, 64, 0, 4, None) == 0 and ws(which, 64, 256, -1, None) == 0
+        assert ws(which, 64, 256, 0, None) == 256
+
+
+def test_gated_refusals():
+    f = n.lib().gptq_fp8_gated_gemm
+
+    def call(A=FAKE, sa=FAKE, M=4, K=256, lda=256, G=FAKE, sg=FAKE, ldg=256, U=FAKE, su=FAKE, ldu=256, N=64, act=0,
+             C=None, dt=0, ldc=0, c=FAKE, ldq=64, s=FAKE, ws=None, wsb=0):
+        return f(A, sa, M, K, lda, G, sg, ldg, U, su, ldu, N, act, C, dt, ldc, c, ldq, s, ws, wsb, None)
+
+    for kw in [dict(A=None), dict(sa=None), dict(G=None), dict(sg=None), dict(U=None), dict(su=None), dict(act=3),
+               dict(act=-1), dict(N=0), dict(K=0), dict(M=-1), dict(lda=255), dict(ldg=255), dict(ldu=255), dict(ldq=63),
+               dict(c=None), dict(s=None), dict(c=None, s=None), dict(C=FAKE, ldc=64), dict(C=FAKE, ldc=63, c=None, s=None),
+               dict(C=FAKE, ldc=64, dt=8, c=None, s=None), dict(su=FAKE + 1), dict(s=FAKE + 2)]:
+        assert call(**kw) == n.ERR_INVALID_ARG, kw
+    need = n.lib().gptq_workspace_bytes(n.WS_FP8_GATED, 64, 256, 4, None)
+    assert call(ws=FAKE, wsb=need - 1) == n.ERR_WORKSPACE
+    assert call(A=None, G=None, U=None, c=None, s=None, M=0) == n.OK
+
+
+# ---------------------------------------------------------------- binding
+def _m(rows, cols, br, dtype=E4):
+    return g.Fp8Matrix(torch.zeros(rows, cols, dtype=torch.uint8).view(dtype),
+                       torch.ones(-(-rows // br), -(-cols // 128)), br)
+
+
+def test_binding_refusals():
+    """Checked before any call: the tensors here are host tensors."""
+    X = torch.zeros(4, 200, dtype=torch.bfloat16)
+    gamma = torch.ones(200, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="block_rows"):
+        g.fp8_quantize(X, 64)
+    with pytest.raises(ValueError, match="dtype"):
+        g.fp8_quantize(X.to(torch.int32))
+    with pytest.raises(ValueError, match="unit column stride"):
+        g.fp8_quantize(X.t())
+    with pytest.raises(ValueError, match="unit column stride"):
+        g.fp8_quantize(X.expand(4, 200)[:1].expand(4, 200))
+    with pytest.raises(ValueError, match="shape"):
+        g.fp8_quantize(X, out=_m(4, 128, 1))
+    with pytest.raises(ValueError, match="device"):
+        g.fp8_quantize(X)
+    for kw, match in [(dict(gamma=gamma[:100]), "shape"), (dict(gamma=gamma.half()), "gamma"),
+                      (dict(residual=X.float()), "residual"), (dict(residual=X[:2]), "residual"),
+                      (dict(h_out=X), "residual"), (dict(want_q=False), "want"),
+                      (dict(residual=X, h_out=X.float()), "h_out")]:
+        with pytest.raises(ValueError, match=match):
+            g.rmsnorm_fp8(X, **{"gamma": gamma, **kw})
+    A, B = _m(4, 256, 1), _m(64, 256, 128)
+    bad = g.Fp8Matrix(A.codes, torch.ones(4, 3), 1)
+    for a, b, kw, match in [(B, B, {}, "block_rows 1"), (A, A, {}, "block_rows 128"), (bad, B, {}, "shape"),
+                            (A, _m(64, 200, 128), {}, "columns"), (A, B, dict(out_dtype=torch.int8), "dtype"),
+                            (A, B, dict(out=torch.zeros(4, 65)), "shape"),
+                            (A, B, dict(out=torch.zeros(4, 64), out_dtype=torch.bfloat16), "out must"),
+                            (g.Fp8Matrix(A.codes.view(torch.uint8), A.scales, 1), B, {}, "float8")]:
+        with pytest.raises(ValueError, match=match):
+            g.fp8_gemm(a, b, **kw)
+    for a, gt, up, kw, match in [(A, B, _m(65, 256, 128), {}, "do not fit"), (A, _m(64, 128, 128), B, {}, "do not fit"),
+                                 (A, B, B, dict(activation="tanh"), "activation"),
+                                 (A, B, B, dict(out=_m(4, 32, 1)), "shape"),
+                                 (A, B, B, dict(out=_m(4, 64, 1), out_dtype=torch.float32), "out_dtype"),
+                                 (A, B, B, dict(out=torch.zeros(4, 32)), "shape")]:
+        with pytest.raises(ValueError, match=match):
+            g.fp8_gated_gemm(a, gt, up, **kw)
