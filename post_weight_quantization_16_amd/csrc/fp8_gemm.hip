@@ -80,10 +80,14 @@ __device__ __forceinline__ i32x4 piece16(const uint8_t* row, int64_t k, int64_t 
   i32x4 v = {0, 0, 0, 0};
   if (ok && k + 16 <= K) {
     __builtin_memcpy(&v, row + k, 16);
-  } else if (ok) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k + i < K) v[i >> 2] |= (int)((uint32_t)row[k + i] << (8 * (i & 3)));
+  } else if (ok && k < K) {
+    uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+    for (int i = 0; i < (int)(K - k); ++i) {
+      const uint64_t x = (uint64_t)row[k + i] << (8 * (i & 7));
+      if (i < 8) lo |= x; else hi |= x;
+    }
+    v = i32x4{(int)(uint32_t)lo, (int)(uint32_t)(lo >> 32), (int)(uint32_t)hi, (int)(uint32_t)(hi >> 32)};
   }
   return v;
 }
@@ -110,12 +114,6 @@ template <int DT> __device__ __forceinline__ void put4(void* C, int64_t at, int 
       if (i < n) p[i] = v[i];
   }
 }
-__device__ __forceinline__ void put4_dt(void* C, int dt, int64_t at, int n, const f32x4& x) {
-  if (dt == GPTQ_F32) put4<GPTQ_F32>(C, at, n, x);
-  else if (dt == GPTQ_BF16) put4<GPTQ_BF16>(C, at, n, x);
-  else put4<GPTQ_F16>(C, at, n, x);
-}
-
 // Magnitudes as integers: finite < infinity < NaN.
 __device__ __forceinline__ uint32_t mag_bits(float x) {
   return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
@@ -124,12 +122,10 @@ __device__ __forceinline__ uint32_t mag_bits(float x) {
 // ---------------------------------------------------------------- tile kernel
 // BM x BN tile of C per workgroup, waves of WM x WN, K in stages of one block
 // in a ring of NS stage buffers.  Stages go from memory straight into LDS
-// (global_load_lds: no registers, no LDS store instructions), NS-1 ahead;
-// a wave waits for its own copies of the next stage, then one barrier
-// publishes everyone's and frees the buffer just read.
+// (global_load_lds: no registers, no LDS store instructions), NS-1 ahead.
 // LDS per stage: BM + BN rows of 128 bytes (16-byte piece p of row r in slot
 // p ^ ((r >> 1) & 7): the 16 rows that a lane group reads together cover all
-// 64 banks), then BM scales of A.
+// 64 banks), then BM scales of A and the tile's one or two scales of B.
 // GATED: the B rows are BN/2 gate rows, then BN/2 up rows of the same
 // columns, and a wave's columns are half gate, half up.
 template <int BM, int BN, int WM, int WN, int NS> struct Tile {
@@ -138,17 +134,20 @@ template <int BM, int BN, int WM, int WN, int NS> struct Tile {
   static constexpr int SEGS = (BM + BN) / 8;            // 1-KB copies per stage
   static constexpr int PER = SEGS / WAVES;              // ... per wave
   static constexpr int NW = PER + 1;                    // with one of 64 scales
-  static constexpr int SB = (BM + BN) * 128 + BM * 4;   // bytes per stage
+  static constexpr int SA = (BM + BN) * 128;            // scales of A, then of B
+  static constexpr int SB = SA + BM * 4 + 256;          // bytes per stage
   static constexpr int SMEM = NS * SB;
-  static_assert(SEGS % WAVES == 0 && WAVES >= BM / 64 && NS >= 2, "copy plan");
-  static_assert((NS - 2) * NW <= 63, "vmcnt range");
+  static_assert(SEGS % WAVES == 0 && WAVES > BM / 64 && BM % 64 == 0 && NS >= 2, "copy plan");
+  static_assert((NS - 2) * NW <= 63 && NS <= 4, "vmcnt range");
 };
 
-constexpr int wait_imm(int n) { return ((n >> 4) << 14) | (n & 15) | 0x70; }   // vmcnt(n), lgkmcnt(0)
-template <int NW> __device__ __forceinline__ void wait_copies(int ahead) {
-  if (ahead <= 0) __builtin_amdgcn_s_waitcnt(wait_imm(0));
-  else if (ahead == 1) __builtin_amdgcn_s_waitcnt(wait_imm(NW));
-  else __builtin_amdgcn_s_waitcnt(wait_imm(2 * NW));
+// Waits until all copies but those of the last `ahead` stages have landed
+// (loads complete in issue order) and this wave's LDS reads are done, then
+// for the other waves.
+template <int NW> __device__ __forceinline__ void stage_barrier(int ahead) {
+  if (ahead <= 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else if (ahead == 1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "i"(NW) : "memory");
+  else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "i"(2 * NW) : "memory");
 }
 
 // Tile of a workgroup.  Workgroup L runs on XCD L % 8: each XCD takes one
@@ -165,7 +164,7 @@ __device__ __forceinline__ void tile_of(uint32_t L, uint32_t total, uint32_t tm,
 
 enum { kStore = 0, kPartial = 1, kCodes = 2 };
 
-template <int BM, int BN, int WM, int WN, int NS, bool FAST, bool GATED, int EPI>
+template <int BM, int BN, int WM, int WN, int NS, bool FAST, bool GATED, int EPI, int DT>
 __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel(GArgs a) {
   using T = Tile<BM, BN, WM, WN, NS>;
   constexpr int MI = T::MI, NI = T::NI, NB = GATED ? 2 : 1;
@@ -181,52 +180,64 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
   const int64_t m0 = (int64_t)bm * BM, n0 = (int64_t)bn * BC;
   const int kbeg = (int)split * a.kper, kend = min(a.kb, kbeg + a.kper);
   const int nst = kend - kbeg;
+  const int mleft = (int)min((int64_t)BM, a.M - m0), nleft = (int)min((int64_t)BC, a.N - n0);
 
-  // copy plan: wave w's copy i fills KB w·PER + i of the stage: rows 8·seg..,
-  // lane l row l/8 of them, slot l%8
-  const uint8_t* src[T::PER];
+  // Copy plan: wave w's copy i fills KB w·PER + i of the stage: eight rows,
+  // lane l row l/8 of them, slot l%8.  Rows past the matrix copy its last
+  // row (their results are never stored).
+  auto seg_base = [&](int seg) -> const uint8_t* {   // wave-uniform
+    if (seg < BM / 8) return a.A + m0 * a.lda;
+    const int half = GATED && seg >= (BM + BC) / 8;
+    return a.B[half] + n0 * a.ldb[half];
+  };
+  auto seg_offset = [&](int seg) -> int64_t {        // this lane's row and piece
+    const int row = seg * 8 + (lane >> 3), p = (lane & 7) ^ ((row >> 1) & 7);
+    if (seg < BM / 8) return (int64_t)min(row, mleft - 1) * a.lda + p * 16;
+    const int half = GATED && seg >= (BM + BC) / 8;
+    return (int64_t)min(row - BM - half * BC, nleft - 1) * a.ldb[half] + p * 16;
+  };
+  uint32_t voff[T::PER];
 #pragma unroll
-  for (int i = 0; i < T::PER; ++i) {
-    const int row = (w * T::PER + i) * 8 + (lane >> 3);
-    const int p = (lane & 7) ^ ((row >> 1) & 7);
-    const uint8_t* base;
-    if (row < BM) {
-      base = a.A + min(m0 + row, a.M - 1) * a.lda;
-    } else {
-      const int br = row - BM, half = GATED ? br / BC : 0;
-      base = a.B[half] + min(n0 + (br - half * BC), a.N - 1) * a.ldb[half];
-    }
-    src[i] = base + (int64_t)kbeg * 128 + p * 16;
+  for (int i = 0; i < T::PER; ++i) voff[i] = (uint32_t)seg_offset(w * T::PER + i);
+  const bool a_scales = w < BM / 64;
+  const float* ssrc;
+  if (a_scales) {
+    ssrc = a.sa + (m0 + min(w * 64 + lane, mleft - 1)) * a.kb;
+  } else {
+    const int q = lane & 1;
+    ssrc = GATED ? a.sb[q] + n0 / 128 * a.kb : a.sb[0] + min(n0 / 128 + q, a.nb - 1) * a.kb;
   }
-  const int srow = (w % (BM / 64)) * 64 + lane;
-  const float* ssrc = a.sa + min(m0 + srow, a.M - 1) * a.kb + kbeg;
+  ssrc += kbeg;
+  const unsigned sdst = T::SA + (a_scales ? w * 256 : BM * 4);
   const unsigned sbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)S;
-  const bool ragged = (a.K & 127) != 0;
+  const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;   // blocks from here on: bytewise
   auto copy = [&](int st) {
-    const unsigned lb = sbase + (unsigned)((st % NS) * T::SB);
-    if (a.wide && !(ragged && kbeg + st == a.kb - 1)) {
+    const unsigned buf = (unsigned)((st % NS) * T::SB);
+    if (kbeg + st < last_wide) {
 #pragma unroll
-      for (int i = 0; i < T::PER; ++i)
-        // 16 bytes per lane from the address to LDS M0 + 16·lane; no register
-        // result, ordered before the reads by the stage waits
-        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
-                     :: "s"(lb + (unsigned)(w * T::PER + i) * 1024u), "v"(src[i] + (int64_t)st * 128)
-                     : "memory");
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
-                   :: "s"(lb + (unsigned)((BM + BN) * 128 + (w % (BM / 64)) * 256)), "v"(ssrc + st)
-                   : "memory");
-    } else {
-      // rows that end inside this block, or that start at odd addresses
-      char* b = S + (st % NS) * T::SB;
       for (int i = 0; i < T::PER; ++i) {
-        const int seg = w * T::PER + i, row = seg * 8 + (lane >> 3);
-        const int p = (lane & 7) ^ ((row >> 1) & 7);
-        const int64_t k = (int64_t)(kbeg + st) * 128 + p * 16;
-        const i32x4 v = piece16(src[i] + (int64_t)st * 128 - k, k, a.K, true);
-        *reinterpret_cast<i32x4*>(b + seg * 1024 + lane * 16) = v;
+        const int seg = w * T::PER + i;
+        // 16 bytes per lane to LDS M0 + 16·lane; no register result, ordered
+        // before the reads by the stage barriers
+        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :: "s"(sbase + buf + (unsigned)seg * 1024u), "v"(voff[i]),
+                        "s"(seg_base(seg) + (int64_t)(kbeg + st) * 128)
+                     : "memory");
       }
-      *reinterpret_cast<float*>(b + (BM + BN) * 128 + srow * 4) = ssrc[st];
-      __builtin_amdgcn_s_waitcnt(wait_imm(0));
+      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
+                   :: "s"(sbase + buf + sdst), "v"(ssrc + st) : "memory");
+    } else {
+      // rows that end inside this block, or start at odd addresses
+#pragma unroll 1
+      for (int i = 0; i < T::PER; ++i) {
+        const int seg = w * T::PER + i;
+        const int64_t off = seg_offset(seg), k = (int64_t)(kbeg + st) * 128;
+        const int p = (lane & 7) ^ (((seg * 8 + (lane >> 3)) >> 1) & 7);
+        const i32x4 v = piece16(seg_base(seg) + off - p * 16, k + p * 16, a.K, true);
+        *reinterpret_cast<i32x4*>(S + buf + seg * 1024 + lane * 16) = v;
+      }
+      *reinterpret_cast<float*>(S + buf + sdst + lane * 4) = ssrc[st];
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
   };
 
@@ -236,64 +247,100 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
 #pragma unroll
     for (int i = 0; i < MI; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const float* sbp[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int64_t blk = min((n0 + wn * WC) / 128, a.nb - 1);
-    sbp[b] = a.sb[b] + blk * a.kb + kbeg;
-  }
   const int l15 = lane & 15, sw = ((lane >> 4) ^ ((l15 >> 1) & 7)) << 4;
   const int arow = (wm * WM + l15) * 128 + sw;
-  int brow[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) brow[b] = (BM + b * BC + wn * WC + l15) * 128 + sw;
-  const int soff = (BM + BN) * 128 + (wm * WM + l15) * 4;
+  const int brow = (BM + wn * WC + l15) * 128 + sw;
+  const int soff = T::SA + (wm * WM + l15) * 4;
+  const int boff = T::SA + BM * 4 + (GATED ? 0 : wn * WC / 128 * 4);
 
-  for (int s0 = 0; s0 < NS - 1 && s0 < nst; ++s0) copy(s0);
-  wait_copies<T::NW>(min(nst - 1, NS - 2));
-  __syncthreads();
-  for (int st = 0; st < nst; ++st) {
-    if (st + NS - 1 < nst) copy(st + NS - 1);
-    const char* b = S + (st % NS) * T::SB;
-    float sb[NB];
+  // Operands of a stage: raw bytes from LDS, then the instruction's form.
+  struct Raw { i32x4 x, y; };
+  auto read_b = [&](const char* b, int j) -> Raw {
+    const int off = brow + (GATED ? (j / (NI / 2)) * BC * 128 + (j % (NI / 2)) * 2048 : j * 2048);
+    return {*reinterpret_cast<const i32x4*>(b + off), *reinterpret_cast<const i32x4*>(b + (off ^ 64))};
+  };
+  auto read_a = [&](const char* b, int i) -> Raw {
+    const int off = arow + i * 2048;
+    return {*reinterpret_cast<const i32x4*>(b + off), *reinterpret_cast<const i32x4*>(b + (off ^ 64))};
+  };
+
+  if (nst > 0) {
+    for (int s0 = 0; s0 < NS - 1 && s0 < nst; ++s0) copy(s0);
+    stage_barrier<T::NW>(min(nst - 1, NS - 2));
+    // The loop is software-pipelined by hand: step (i, j) multiplies A piece i
+    // by B piece j and adds the product of the step before, so the matrix
+    // core works while the adds run; A pieces are read one ahead, and the
+    // next stage's first pieces after the barrier that is placed before the
+    // last A piece's steps.
+    Frag<FAST> fb[NI], fa;
+    Raw ra;
+    float sb[NB], sa, sn;
 #pragma unroll
-    for (int q = 0; q < NB; ++q) sb[q] = sbp[q][st];
-    Frag<FAST> fb[NI];
+    for (int j = 0; j < NI; ++j) { const Raw r = read_b(S, j); fb[j].set(r.x, r.y); }
+    ra = read_a(S, 0);
+    sn = *reinterpret_cast<const float*>(S + soff);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int off = brow[GATED ? j / (NI / 2) : 0] + (GATED ? j % (NI / 2) : j) * 2048;
-      fb[j].set(*reinterpret_cast<const i32x4*>(b + off), *reinterpret_cast<const i32x4*>(b + (off ^ 64)));
-    }
+    for (int q = 0; q < NB; ++q) sb[q] = *reinterpret_cast<const float*>(S + boff + 4 * q);
+    for (int st = 0; st < nst; ++st) {
+      if (st + NS - 1 < nst) copy(st + NS - 1);
+      const char* b = S + (st % NS) * T::SB;
+      const char* bn_ = S + ((st + 1) % NS) * T::SB;
+      f32x4 p;
+      float sp = 0.f, s[NB];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      Frag<FAST> fa;
-      const int off = arow + i * 2048;
-      fa.set(*reinterpret_cast<const i32x4*>(b + off), *reinterpret_cast<const i32x4*>(b + (off ^ 64)));
-      const float sa = *reinterpret_cast<const float*>(b + soff + i * 64);
+      for (int i = 0; i < MI; ++i) {
+        fa.set(ra.x, ra.y);
+        sa = sn;
 #pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        const f32x4 p = contract(fb[j], fa);
-        const float s = sa * sb[GATED ? j / (NI / 2) : 0];
+        for (int q = 0; q < NB; ++q) s[q] = sa * sb[q];
+        if (i + 1 < MI) {
+          ra = read_a(b, i + 1);
+          sn = *reinterpret_cast<const float*>(b + soff + (i + 1) * 64);
+        } else {
+          stage_barrier<T::NW>(min(nst - 1, st + NS - 1) - (st + 1));
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[j][i][r] = __builtin_fmaf(p[r], s, acc[j][i][r]);
+        for (int j = 0; j < NI; ++j) {
+          const f32x4 q = contract(fb[j], fa);
+          if (i + 1 == MI) {   // the next stage's pieces (past the last stage: unused bytes)
+            const Raw r = read_b(bn_, j);
+            fb[j].set(r.x, r.y);
+            if (j == 0) {
+              ra = read_a(bn_, 0);
+              sn = *reinterpret_cast<const float*>(bn_ + soff);
+#pragma unroll
+              for (int h = 0; h < NB; ++h) sb[h] = *reinterpret_cast<const float*>(bn_ + boff + 4 * h);
+            }
+          }
+          const int pi = j > 0 ? i : i - 1, pj = j > 0 ? j - 1 : NI - 1;
+          if (pi >= 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[pj][pi][r] = __builtin_fmaf(p[r], sp, acc[pj][pi][r]);
+          }
+          p = q;
+          sp = s[GATED ? j / (NI / 2) : 0];
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        acc[NI - 1][MI - 1][r] = __builtin_fmaf(p[r], sp, acc[NI - 1][MI - 1][r]);
     }
-    wait_copies<T::NW>(min(nst - 1, st + NS - 1) - (st + 1));
-    __syncthreads();
+    __syncthreads();   // the epilogue reuses the stage buffers
   }
 
+  const int nl = wn * WC + 4 * (lane >> 4);   // this lane's first column in the tile
   if constexpr (EPI == kPartial) {
     float* P = a.P + (int64_t)split * NB * a.M * a.N;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int64_t m = m0 + wm * WM + i * 16 + l15;
-      if (m >= a.M) continue;
+      const int ml = wm * WM + i * 16 + l15;
+      if (ml >= mleft) continue;
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
-        const int half = GATED ? j / (NI / 2) : 0;
-        const int64_t n = n0 + wn * WC + (GATED ? j % (NI / 2) : j) * 16 + 4 * (lane >> 4);
-        if (n < a.N)
-          put4<GPTQ_F32>(P, ((int64_t)half * a.M + m) * a.N + n, (int)min((int64_t)4, a.N - n), acc[j][i]);
+        const int half = GATED ? j / (NI / 2) : 0, c = nl + (GATED ? j % (NI / 2) : j) * 16;
+        put4<GPTQ_F32>(P, ((int64_t)half * a.M + m0 + ml) * a.N + n0 + c, nleft - c, acc[j][i]);
       }
     }
     return;
@@ -310,13 +357,11 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
   if constexpr (EPI == kStore) {
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int64_t m = m0 + wm * WM + i * 16 + l15;
-      if (m >= a.M) continue;
+      const int ml = wm * WM + i * 16 + l15;
+      if (ml >= mleft) continue;
 #pragma unroll
-      for (int j = 0; j < NO; ++j) {
-        const int64_t n = n0 + wn * WC + j * 16 + 4 * (lane >> 4);
-        if (n < a.N) put4_dt(a.C, a.c_dt, m * a.ldc + n, (int)min((int64_t)4, a.N - n), acc[j][i]);
-      }
+      for (int j = 0; j < NO; ++j)
+        put4<DT>(a.C, (m0 + ml) * a.ldc + n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
     }
   } else {
     // the tile's 128 columns are one block of its rows
@@ -328,10 +373,8 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
 #pragma unroll
       for (int j = 0; j < NO; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int64_t n = n0 + wn * WC + j * 16 + 4 * (lane >> 4) + r;
-          if (n < a.N) u = max(u, mag_bits(acc[j][i][r]));
-        }
+        for (int r = 0; r < 4; ++r)
+          if (nl + j * 16 + r < nleft) u = max(u, mag_bits(acc[j][i][r]));
       u = max(u, (uint32_t)__shfl_xor((int)u, 16));
       u = max(u, (uint32_t)__shfl_xor((int)u, 32));
       if (lane < 16) top[wn * BM + wm * WM + i * 16 + l15] = u;
@@ -339,28 +382,28 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int64_t m = m0 + wm * WM + i * 16 + l15;
+      const int ml = wm * WM + i * 16 + l15;
       uint32_t u = 0;
 #pragma unroll
-      for (int q = 0; q < BN / WN; ++q) u = max(u, top[q * BM + wm * WM + i * 16 + l15]);
+      for (int q = 0; q < BN / WN; ++q) u = max(u, top[q * BM + ml]);
       const float s = e4m3_scale((double)__builtin_bit_cast(float, u));
       const double sd = (double)s, inv = 1.0 / sd;
-      if (m >= a.M) continue;
-      if (wn == 0 && lane < 16) a.sc[m * a.nb + bn] = s;
+      if (ml >= mleft) continue;
+      if (wn == 0 && lane < 16) a.sc[(m0 + ml) * a.nb + bn] = s;
 #pragma unroll
       for (int j = 0; j < NO; ++j) {
-        const int64_t n = n0 + wn * WC + j * 16 + 4 * (lane >> 4);
         float q[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) q[r] = e4m3_quotient((double)acc[j][i][r], sd, inv);
         const uint32_t c = e4m3_pack4(q[0], q[1], q[2], q[3]);
-        uint8_t* p = a.codes + m * a.ld_codes + n;
-        if (n + 4 <= a.N) {
-          __builtin_memcpy(p, &c, 4);
+        uint8_t* o = a.codes + (m0 + ml) * a.ld_codes + n0 + nl + j * 16;
+        const int n = nleft - nl - j * 16;
+        if (n >= 4) {
+          __builtin_memcpy(o, &c, 4);
         } else {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (n + r < a.N) p[r] = (uint8_t)(c >> (8 * r));
+            if (r < n) o[r] = (uint8_t)(c >> (8 * r));
         }
       }
     }
@@ -542,28 +585,32 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool ws) {
   return p;
 }
 
-template <int BM, int BN, int WM, int WN, int NS, bool FAST, bool GATED, int EPI>
+template <int BM, int BN, int WM, int WN, int NS, bool FAST, bool GATED, int EPI, int DT>
 hipError_t launch_tile(GArgs& a, int splits, hipStream_t s) {
   using T = Tile<BM, BN, WM, WN, NS>;
   a.tm = (int)ceil_div(a.M, BM);
   a.tn = (int)ceil_div(a.N, GATED ? BN / 2 : BN);
   const int64_t grid = (int64_t)a.tm * a.tn * splits;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  tile_kernel<BM, BN, WM, WN, NS, FAST, GATED, EPI><<<(unsigned)grid, T::NT, 0, s>>>(a);
+  tile_kernel<BM, BN, WM, WN, NS, FAST, GATED, EPI, DT><<<(unsigned)grid, T::NT, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <bool GATED, bool FAST>
+// One output form: EPI with DT (FAST goes with the 16-bit types).
+template <bool GATED, int EPI, int DT>
 hipError_t run(GArgs& a, void* ws, hipStream_t s) {
+  constexpr bool FAST = EPI == kStore && DT != GPTQ_F32;
   const Plan p = plan_of(a.M, a.N, a.K, GATED, ws != nullptr);
   a.nb = ceil_div(a.N, 128);
   a.kb = (int)ceil_div(a.K, 128);
   a.kper = p.kper;
   a.P = static_cast<float*>(ws);
-  a.wide = (uintptr_t)a.A % 16 == 0 && (a.M == 1 || a.lda % 16 == 0);
-  for (int b = 0; b < (GATED ? 2 : 1); ++b)
-    a.wide = a.wide && (uintptr_t)a.B[b] % 16 == 0 && (a.N == 1 || a.ldb[b] % 16 == 0);
-  const bool codes = GATED && a.codes;
+  // the wide copies' 32-bit offsets span a tile's rows
+  auto wide = [](const uint8_t* q, int64_t rows, int64_t ld) {
+    return (uintptr_t)q % 16 == 0 && (rows == 1 || (ld % 16 == 0 && ld < ((int64_t)1 << 23)));
+  };
+  a.wide = wide(a.A, a.M, a.lda) && wide(a.B[0], a.N, a.ldb[0]) && (!GATED || wide(a.B[1], a.N, a.ldb[1]));
+  constexpr bool codes = EPI == kCodes;
   hipError_t e;
   if (p.few && !(codes && !ws)) {
     const unsigned grid = (unsigned)ceil_div(a.N, 16);
@@ -577,23 +624,22 @@ hipError_t run(GArgs& a, void* ws, hipStream_t s) {
     return hipGetLastError();
   }
   if (p.splits > 1) {
-    e = GATED ? launch_tile<128, 256, 64, 64, 2, FAST, GATED, kPartial>(a, p.splits, s)
-              : launch_tile<128, 128, 64, 64, 2, FAST, GATED, kPartial>(a, p.splits, s);
+    e = launch_tile<128, GATED ? 256 : 128, 64, 64, 2, FAST, GATED, kPartial, GPTQ_F32>(a, p.splits, s);
     if (e != hipSuccess) return e;
-    const int64_t grid = ceil_div(a.M * a.nb, 16);
-    if (codes) join_kernel<GATED, true><<<(unsigned)grid, 256, 0, s>>>(a, p.splits);
-    else join_kernel<GATED, false><<<(unsigned)grid, 256, 0, s>>>(a, p.splits);
+    join_kernel<GATED, codes><<<(unsigned)ceil_div(a.M * a.nb, 16), 256, 0, s>>>(a, p.splits);
     return hipGetLastError();
   }
-  if constexpr (GATED) {
-    if (p.bm == 256)
-      return codes ? launch_tile<256, 256, 128, 64, 2, FAST, true, kCodes>(a, 1, s)
-                   : launch_tile<256, 256, 128, 64, 2, FAST, true, kStore>(a, 1, s);
-    return codes ? launch_tile<128, 256, 64, 64, 2, FAST, true, kCodes>(a, 1, s)
-                 : launch_tile<128, 256, 64, 64, 2, FAST, true, kStore>(a, 1, s);
-  } else {
-    return p.bm == 256 ? launch_tile<256, 256, 128, 64, 2, FAST, false, kStore>(a, 1, s)
-                       : launch_tile<128, 128, 64, 64, 2, FAST, false, kStore>(a, 1, s);
+  if (p.bm == 256) return launch_tile<256, 256, 128, 64, 2, FAST, GATED, EPI, DT>(a, 1, s);
+  return launch_tile<128, GATED ? 256 : 128, 64, 64, 2, FAST, GATED, EPI, DT>(a, 1, s);
+}
+
+template <bool GATED> hipError_t run_dt(GArgs& a, void* ws, hipStream_t s) {
+  if constexpr (GATED)
+    if (a.codes) return run<true, kCodes, GPTQ_F32>(a, ws, s);
+  switch (a.c_dt) {
+    case GPTQ_F32: return run<GATED, kStore, GPTQ_F32>(a, ws, s);
+    case GPTQ_BF16: return run<GATED, kStore, GPTQ_BF16>(a, ws, s);
+    default: return run<GATED, kStore, GPTQ_F16>(a, ws, s);
   }
 }
 
@@ -615,7 +661,7 @@ hipError_t fp8_gemm_launch(const uint8_t* A, const float* sa, int64_t M, int64_t
   a.A = A; a.sa = sa; a.M = M; a.K = K; a.lda = lda;
   a.B[0] = B; a.sb[0] = sb; a.N = N; a.ldb[0] = ldb;
   a.C = C; a.ldc = ldc; a.c_dt = c_dt;
-  return c_dt == GPTQ_F32 ? run<false, false>(a, ws, s) : run<false, true>(a, ws, s);
+  return run_dt<false>(a, ws, s);
 }
 
 hipError_t fp8_gated_launch(const uint8_t* A, const float* sa, int64_t M, int64_t K, int64_t lda,
@@ -629,7 +675,7 @@ hipError_t fp8_gated_launch(const uint8_t* A, const float* sa, int64_t M, int64_
   a.B[1] = U; a.sb[1] = su; a.ldb[1] = ldu; a.N = N;
   a.C = C; a.ldc = ldc; a.c_dt = c_dt; a.act = act;
   a.codes = codes; a.ld_codes = ld_codes; a.sc = sc;
-  return codes || c_dt == GPTQ_F32 ? run<true, false>(a, ws, s) : run<true, true>(a, ws, s);
+  return run_dt<true>(a, ws, s);
 }
 
 }  // namespace gq
