@@ -302,7 +302,10 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
-          const f32x4 q = contract(fb[j], fa);
+          f32x4 q = contract(fb[j], fa);
+          // keeps the adds below behind this product
+          if (i + j > 0) asm volatile("" : "+v"(q), "+v"(p));
+          else asm volatile("" : "+v"(q));
           if (i + 1 == MI) {   // the next stage's pieces (past the last stage: unused bytes)
             const Raw r = read_b(bn_, j);
             fb[j].set(r.x, r.y);
