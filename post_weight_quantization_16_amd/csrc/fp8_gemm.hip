@@ -125,7 +125,10 @@ __device__ __forceinline__ uint32_t mag_bits(float x) {
 // (global_load_lds: no registers, no LDS store instructions), NS-1 ahead.
 // LDS per stage: BM + BN rows of 128 bytes (16-byte piece p of row r in slot
 // p ^ ((r >> 1) & 7): the 16 rows that a lane group reads together cover all
-// 64 banks), then BM scales of A and the tile's one or two scales of B.
+// 64 banks).  Scales come eight blocks of K at a time, 8 rows x 8 blocks a
+// copy (a copy of one block's scales touches a cache line for each row: with
+// those, 4096 x 28672 x 8192 took 917 us instead of 843), into two buffers of
+// [BM + 2][8]: the rows of A, then the tile's one or two blocks of B.
 // GATED: the B rows are BN/2 gate rows, then BN/2 up rows of the same
 // columns, and a wave's columns are half gate, half up.
 template <int BM, int BN, int WM, int WN, int NS> struct Tile {
@@ -133,17 +136,20 @@ template <int BM, int BN, int WM, int WN, int NS> struct Tile {
   static constexpr int MI = WM / 16, NI = WN / 16;
   static constexpr int SEGS = (BM + BN) / 8;            // 1-KB copies per stage
   static constexpr int PER = SEGS / WAVES;              // ... per wave
-  static constexpr int NW = PER + 1;                    // with one of 64 scales
-  static constexpr int SA = (BM + BN) * 128;            // scales of A, then of B
-  static constexpr int SB = SA + BM * 4 + 256;          // bytes per stage
-  static constexpr int SMEM = NS * SB;
-  static_assert(SEGS % WAVES == 0 && WAVES > BM / 64 && BM % 64 == 0 && NS >= 2, "copy plan");
-  static_assert((NS - 2) * NW <= 63 && NS <= 4, "vmcnt range");
+  static constexpr int SB = (BM + BN) * 128;            // bytes per stage
+  static constexpr int SCALES = NS * SB;                // two buffers of scales
+  static constexpr int SCB = BM * 32 + 256;
+  static constexpr int SMEM = SCALES + 2 * SCB;
+  static constexpr int SCOPIES = BM / 8 + 1;            // copies of eight blocks' scales
+  static_assert(SEGS % WAVES == 0 && NS >= 2 && NS <= 4, "copy plan");
+  // issued over the stages of the eight blocks before, the last of them early
+  // enough for the stage barriers to cover them
+  static_assert(SCOPIES <= (8 - NS + 1) * WAVES && (NS - 2) * PER <= 63, "copy plan");
 };
 
-// Waits until all copies but those of the last `ahead` stages have landed
-// (loads complete in issue order) and this wave's LDS reads are done, then
-// for the other waves.
+// Waits until all copies but the last `ahead` stages' (loads complete in issue
+// order; copies of scales among them only make the wait longer) have landed
+// and this wave's LDS reads are done, then for the other waves.
 template <int NW> __device__ __forceinline__ void stage_barrier(int ahead) {
   if (ahead <= 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   else if (ahead == 1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "i"(NW) : "memory");
@@ -190,53 +196,58 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
     const int half = GATED && seg >= (BM + BC) / 8;
     return a.B[half] + n0 * a.ldb[half];
   };
-  auto seg_offset = [&](int seg) -> int64_t {        // this lane's row and piece
-    const int row = seg * 8 + (lane >> 3), p = (lane & 7) ^ ((row >> 1) & 7);
-    if (seg < BM / 8) return (int64_t)min(row, mleft - 1) * a.lda + p * 16;
+  auto seg_offset = [&](int seg, int l) -> int64_t {   // row and piece of lane l
+    const int row = seg * 8 + (l >> 3), p16 = (((l & 7) ^ (l >> 4)) << 4) ^ ((seg & 1) << 6);
+    if (seg < BM / 8) return (int64_t)min(row, mleft - 1) * a.lda + p16;
     const int half = GATED && seg >= (BM + BC) / 8;
-    return (int64_t)min(row - BM - half * BC, nleft - 1) * a.ldb[half] + p * 16;
+    return (int64_t)min(row - BM - half * BC, nleft - 1) * a.ldb[half] + p16;
   };
-  uint32_t voff[T::PER];
+  // The exact form has no registers left to keep its offsets in (a spill
+  // would wait for the copies in flight) and computes them anew each stage.
+  uint32_t voff[FAST ? T::PER : 1];
+  if constexpr (FAST) {
 #pragma unroll
-  for (int i = 0; i < T::PER; ++i) voff[i] = (uint32_t)seg_offset(w * T::PER + i);
-  const bool a_scales = w < BM / 64;
-  const float* ssrc;
-  if (a_scales) {
-    ssrc = a.sa + (m0 + min(w * 64 + lane, mleft - 1)) * a.kb;
-  } else {
-    const int q = lane & 1;
-    ssrc = GATED ? a.sb[q] + n0 / 128 * a.kb : a.sb[0] + min(n0 / 128 + q, a.nb - 1) * a.kb;
+    for (int i = 0; i < T::PER; ++i) voff[i] = (uint32_t)seg_offset(w * T::PER + i, lane);
   }
-  ssrc += kbeg;
-  const unsigned sdst = T::SA + (a_scales ? w * 256 : BM * 4);
   const unsigned sbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)S;
   const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;   // blocks from here on: bytewise
+  // copy `idx` of the scales of blocks 8·g.. of this split
+  auto copy_scales = [&](int g, int idx) {
+    int l = lane;
+    if constexpr (!FAST) asm volatile("" : "+v"(l));   // not hoisted
+    const int r = l >> 3, k = min(kbeg + 8 * g + (l & 7), a.kb - 1);
+    const float* p;
+    if (idx < BM / 8) p = a.sa + (m0 + min(idx * 8 + r, mleft - 1)) * a.kb;
+    else if (GATED) p = (r == 0 ? a.sb[0] : a.sb[NB - 1]) + n0 / 128 * a.kb;
+    else p = a.sb[0] + min(n0 / 128 + min(r, 1), a.nb - 1) * a.kb;
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
+                 :: "s"(sbase + T::SCALES + (unsigned)((g & 1) * T::SCB + idx * 256)), "v"(p + k) : "memory");
+  };
   auto copy = [&](int st) {
     const unsigned buf = (unsigned)((st % NS) * T::SB);
     if (kbeg + st < last_wide) {
+      int l = lane;
+      if constexpr (!FAST) asm volatile("" : "+v"(l));   // not hoisted
 #pragma unroll
       for (int i = 0; i < T::PER; ++i) {
         const int seg = w * T::PER + i;
         // 16 bytes per lane to LDS M0 + 16·lane; no register result, ordered
         // before the reads by the stage barriers
         asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
-                     :: "s"(sbase + buf + (unsigned)seg * 1024u), "v"(voff[i]),
+                     :: "s"(sbase + buf + (unsigned)seg * 1024u), "v"(FAST ? voff[FAST ? i : 0] : (uint32_t)seg_offset(seg, l)),
                         "s"(seg_base(seg) + (int64_t)(kbeg + st) * 128)
                      : "memory");
       }
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
-                   :: "s"(sbase + buf + sdst), "v"(ssrc + st) : "memory");
     } else {
       // rows that end inside this block, or start at odd addresses
 #pragma unroll 1
       for (int i = 0; i < T::PER; ++i) {
         const int seg = w * T::PER + i;
-        const int64_t off = seg_offset(seg), k = (int64_t)(kbeg + st) * 128;
-        const int p = (lane & 7) ^ (((seg * 8 + (lane >> 3)) >> 1) & 7);
-        const i32x4 v = piece16(seg_base(seg) + off - p * 16, k + p * 16, a.K, true);
+        const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((seg & 1) << 6);
+        const int64_t k = (int64_t)(kbeg + st) * 128 + p16;
+        const i32x4 v = piece16(seg_base(seg) + seg_offset(seg, lane) - p16, k, a.K, true);
         *reinterpret_cast<i32x4*>(S + buf + seg * 1024 + lane * 16) = v;
       }
-      *reinterpret_cast<float*>(S + buf + sdst + lane * 4) = ssrc[st];
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
   };
@@ -250,8 +261,9 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
   const int l15 = lane & 15, sw = ((lane >> 4) ^ ((l15 >> 1) & 7)) << 4;
   const int arow = (wm * WM + l15) * 128 + sw;
   const int brow = (BM + wn * WC + l15) * 128 + sw;
-  const int soff = T::SA + (wm * WM + l15) * 4;
-  const int boff = T::SA + BM * 4 + (GATED ? 0 : wn * WC / 128 * 4);
+  const int soff = T::SCALES + (wm * WM + l15) * 32;
+  const int boff = T::SCALES + BM * 32 + (GATED ? 0 : wn * WC / 128 * 32);
+  auto scales_of = [&](int st) { return S + ((st >> 3) & 1) * T::SCB + (st & 7) * 4; };
 
   // Operands of a stage: raw bytes from LDS, then the instruction's form.
   struct Raw { i32x4 x, y; };
@@ -265,8 +277,9 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
   };
 
   if (nst > 0) {
+    for (int i = w; i < T::SCOPIES; i += T::WAVES) copy_scales(0, i);
     for (int s0 = 0; s0 < NS - 1 && s0 < nst; ++s0) copy(s0);
-    stage_barrier<T::NW>(min(nst - 1, NS - 2));
+    stage_barrier<T::PER>(min(nst - 1, NS - 2));
     // The loop is software-pipelined by hand: step (i, j) multiplies A piece i
     // by B piece j and adds the product of the step before, so the matrix
     // core works while the adds run; A pieces are read one ahead, and the
@@ -280,9 +293,15 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
     ra = read_a(S, 0);
     sn = *reinterpret_cast<const float*>(S + soff);
 #pragma unroll
-    for (int q = 0; q < NB; ++q) sb[q] = *reinterpret_cast<const float*>(S + boff + 4 * q);
+    for (int q = 0; q < NB; ++q) sb[q] = *reinterpret_cast<const float*>(S + boff + 32 * q);
     for (int st = 0; st < nst; ++st) {
       if (st + NS - 1 < nst) copy(st + NS - 1);
+      {
+        const int i = (st & 7) * T::WAVES + w;
+        if (i < T::SCOPIES && (st | 7) + 1 < nst) copy_scales((st >> 3) + 1, i);
+      }
+      const char* sc = scales_of(st);
+      const char* sc_ = scales_of(st + 1);
       const char* b = S + (st % NS) * T::SB;
       const char* bn_ = S + ((st + 1) % NS) * T::SB;
       f32x4 p;
@@ -295,9 +314,9 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
         for (int q = 0; q < NB; ++q) s[q] = sa * sb[q];
         if (i + 1 < MI) {
           ra = read_a(b, i + 1);
-          sn = *reinterpret_cast<const float*>(b + soff + (i + 1) * 64);
+          sn = *reinterpret_cast<const float*>(sc + soff + (i + 1) * 512);
         } else {
-          stage_barrier<T::NW>(min(nst - 1, st + NS - 1) - (st + 1));
+          stage_barrier<T::PER>(min(nst - 1, st + NS - 1) - (st + 1));
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -311,15 +330,16 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
             fb[j].set(r.x, r.y);
             if (j == 0) {
               ra = read_a(bn_, 0);
-              sn = *reinterpret_cast<const float*>(bn_ + soff);
+              sn = *reinterpret_cast<const float*>(sc_ + soff);
 #pragma unroll
-              for (int h = 0; h < NB; ++h) sb[h] = *reinterpret_cast<const float*>(bn_ + boff + 4 * h);
+              for (int h = 0; h < NB; ++h) sb[h] = *reinterpret_cast<const float*>(sc_ + boff + 32 * h);
             }
           }
           const int pi = j > 0 ? i : i - 1, pj = j > 0 ? j - 1 : NI - 1;
           if (pi >= 0) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[pj][pi][r] = __builtin_fmaf(p[r], sp, acc[pj][pi][r]);
+            asm volatile("" : "+v"(acc[pj][pi]));   // ... and here
           }
           p = q;
           sp = s[GATED ? j / (NI / 2) : 0];
