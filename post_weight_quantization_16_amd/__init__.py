@@ -534,80 +534,108 @@ class Normed:
     y: "object"          # [rows, cols] y in x's type, or None
 
 
-def _fp8_codes(rows: int, cols: int, device):
-    """Codes whose rows start at multiples of 16 bytes (what the products'
-    wide copies need); the bytes behind a row's end are not written."""
-    torch = _torch()
+_T = None   # what the 8-bit calls need of torch, looked up once
+
+
+def _t8():
+    global _T
+    if _T is None:
+        torch = _torch()
+        _T = (torch.empty, torch.float8_e4m3fn, torch.float32, torch.cuda.current_device,
+              torch._C._cuda_getCurrentRawStream,
+              {torch.float32: _native.F32, torch.bfloat16: _native.BF16, torch.float16: _native.F16})
+    return _T
+
+
+def _fp8_new(rows: int, cols: int, block_rows: int, device) -> tuple:
+    """(Fp8Matrix, row stride) to be filled.  Its rows start at multiples of
+    16 bytes (what the products' wide copies need); the bytes behind a row's
+    end are not written."""
+    empty, e4m3, f32 = _t8()[:3]
     ld = (cols + 15) // 16 * 16
-    c = torch.empty(rows, ld, dtype=torch.float8_e4m3fn, device=device)
-    return c if ld == cols else c[:, :cols]
+    c = empty((rows, ld), dtype=e4m3, device=device)
+    s = empty(((rows + block_rows - 1) // block_rows, (cols + FP8_BLOCK - 1) // FP8_BLOCK), dtype=f32,
+              device=device)
+    return Fp8Matrix(c if ld == cols else c[:, :cols], s, block_rows), ld
 
 
 def _fp8_arg(m: Fp8Matrix, name, block_rows, device=None):
-    """(rows, cols, row stride) of a block-scaled argument after its checks."""
-    torch = _torch()
+    """(rows, cols, row stride, device) of a block-scaled argument after its checks."""
     if m.block_rows != block_rows:
         raise ValueError(f"{name} must have block_rows {block_rows} (got {m.block_rows})")
     c, s = m.codes, m.scales
-    if c.dtype != torch.float8_e4m3fn:
+    _, e4m3, f32 = _t8()[:3]
+    if c.dtype != e4m3:
         raise ValueError(f"{name}.codes must be float8_e4m3fn (got {c.dtype})")
-    ld = _fp8_rows(c, f"{name}.codes")
+    ld = _fp8_rows(c, name)
     rows, cols = c.shape
-    _require(s, f"{name}.scales", torch.float32,
-             ((rows + block_rows - 1) // block_rows, (cols + FP8_BLOCK - 1) // FP8_BLOCK), c.device)
-    if device is not None and c.device != device:
-        raise ValueError(f"{name} is on {c.device}, expected {device}")
-    return rows, cols, ld
+    dev = c.device
+    want = ((rows + block_rows - 1) // block_rows, (cols + FP8_BLOCK - 1) // FP8_BLOCK)
+    if s.dtype != f32 or s.shape != want or not s.is_contiguous():
+        raise ValueError(f"{name}.scales must be contiguous float32 of shape {want} "
+                         f"(got {s.dtype}, {tuple(s.shape)})")
+    if s.device != dev or (device is not None and dev != device):
+        raise ValueError(f"{name} is on {dev} (scales on {s.device}), expected {device or dev}")
+    return rows, cols, ld, dev
 
 
 def _fp8_rows(t, name) -> int:
     """Row stride of a 2-D tensor with unit column stride (a single row's own
     stride says nothing: its length is taken)."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with unit column stride")
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    if t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name} must be 2-D with unit column stride")
-    return t.stride(0)
+    st = t.stride()
+    if len(st) == 2:
+        rows, cols = t.shape
+        if st[1] == 1 or cols <= 1:
+            if rows <= 1:
+                return cols
+            if st[0] >= cols:
+                return st[0]
+    raise ValueError(f"{name} must be 2-D with unit column stride")
+
+
+def _fp8_dtype(t, name) -> int:
+    code = _t8()[5].get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: unsupported dtype {t.dtype} (float32, bfloat16 or float16)")
+    return code
 
 
 def _fp8_out(t, name, dtype, shape, device) -> int:
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+    if t.dtype != dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be {dtype} of shape {shape} on {device}")
     return _fp8_rows(t, name)
 
 
 def _launch(device, fn, *args):
     """Call an entry point with the device current and its stream last."""
-    torch = _torch()
-    if not device.type == "cuda":
+    if device.type != "cuda":
         raise ValueError("the tensors must be device tensors")
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    i = device.index
+    _, _, _, current, raw_stream, _ = _t8()
+    if current() == i:
+        rc = fn(*args, raw_stream(i))
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+        with _torch().cuda.device(i):
+            rc = fn(*args, raw_stream(i))
+    if rc != _native.OK:
+        _check(rc)
 
 
 def fp8_quantize(X, block_rows: int = 1, out: Fp8Matrix | None = None) -> Fp8Matrix:
     """X [rows, cols] (float32/bfloat16/float16) in e4m3 with one scale per
     block of block_rows x 128: 1 for activations, 128 for weights."""
-    torch = _torch()
-    xdt = _dtype_code(X)
+    xdt = _fp8_dtype(X, "X")
     ld_x = _fp8_rows(X, "X")
     rows, cols = X.shape
     dev = X.device
     if block_rows not in (1, FP8_BLOCK):
         raise ValueError(f"block_rows must be 1 or {FP8_BLOCK} (got {block_rows})")
     if out is None:
-        out = Fp8Matrix(_fp8_codes(rows, cols, dev),
-                        torch.empty((rows + block_rows - 1) // block_rows,
-                                    (cols + FP8_BLOCK - 1) // FP8_BLOCK, dtype=torch.float32,
-                                    device=dev), block_rows)
-    r, c, ld_c = _fp8_arg(out, "out", block_rows, dev)
-    if (r, c) != (rows, cols):
-        raise ValueError(f"out must have shape {(rows, cols)} (got {(r, c)})")
+        out, ld_c = _fp8_new(rows, cols, block_rows, dev)
+    else:
+        r, c, ld_c, _ = _fp8_arg(out, "out", block_rows, dev)
+        if (r, c) != (rows, cols):
+            raise ValueError(f"out must have shape {(rows, cols)} (got {(r, c)})")
     _launch(dev, _native.lib().gptq_fp8_quantize, X.data_ptr(), xdt, rows, cols, ld_x, block_rows,
             out.codes.data_ptr(), ld_c, out.scales.data_ptr())
     return out
@@ -619,42 +647,46 @@ def rmsnorm_fp8(X, gamma, eps: float = 1e-6, residual=None, want_q: bool = True,
     per row, quantized in 1 x 128 blocks (want_q) and/or rounded to X's type
     (want_y).  h_out: where h goes (X or residual itself for an update in
     place); without a residual h is X and nothing is written."""
-    torch = _torch()
-    xdt = _dtype_code(X)
+    empty, _, f32 = _t8()[:3]
+    xdt = _fp8_dtype(X, "X")
     ld_x = _fp8_rows(X, "X")
     rows, cols = X.shape
     dev = X.device
-    if gamma.dtype not in (X.dtype, torch.float32):
-        raise ValueError(f"gamma must be {X.dtype} or float32 (got {gamma.dtype})")
-    _require(gamma, "gamma", gamma.dtype, (cols,), dev)
+    dt = X.dtype
+    if gamma.dtype != dt and gamma.dtype != f32:
+        raise ValueError(f"gamma must be {dt} or float32 (got {gamma.dtype})")
+    if gamma.shape != (cols,) or not gamma.is_contiguous() or gamma.device != dev:
+        raise ValueError(f"gamma must be contiguous of shape {(cols,)} on {dev}")
     if not (want_q or want_y):
         raise ValueError("want_q or want_y must be set")
     h, ld_r, ld_h, hp = X, 0, 0, None
     if residual is not None:
-        ld_r = _fp8_out(residual, "residual", X.dtype, (rows, cols), dev)
-        h = torch.empty(rows, cols, dtype=X.dtype, device=dev) if h_out is None else h_out
-        ld_h = _fp8_out(h, "h_out", X.dtype, (rows, cols), dev)
+        ld_r = _fp8_out(residual, "residual", dt, (rows, cols), dev)
+        h = empty((rows, cols), dtype=dt, device=dev) if h_out is None else h_out
+        ld_h = cols if h_out is None else _fp8_out(h, "h_out", dt, (rows, cols), dev)
         hp = h.data_ptr()
     elif h_out is not None:
         raise ValueError("h_out needs a residual")
-    y = torch.empty(rows, cols, dtype=X.dtype, device=dev) if want_y else None
+    y = empty((rows, cols), dtype=dt, device=dev) if want_y else None
     q, qc, qs, ld_c = None, None, None, 0
     if want_q:
-        q = Fp8Matrix(_fp8_codes(rows, cols, dev),
-                      torch.empty(rows, (cols + FP8_BLOCK - 1) // FP8_BLOCK, dtype=torch.float32,
-                                  device=dev), 1)
-        qc, qs, ld_c = q.codes.data_ptr(), q.scales.data_ptr(), (cols + 15) // 16 * 16
+        q, ld_c = _fp8_new(rows, cols, 1, dev)
+        qc, qs = q.codes.data_ptr(), q.scales.data_ptr()
     _launch(dev, _native.lib().gptq_rmsnorm_fp8, X.data_ptr(), ld_x,
             None if residual is None else residual.data_ptr(), ld_r, xdt, gamma.data_ptr(),
-            _dtype_code(gamma), rows, cols, eps, hp, ld_h, y.data_ptr() if want_y else None, cols,
-            qc, ld_c, qs)
+            xdt if gamma.dtype == dt else _native.F32, rows, cols, eps, hp, ld_h,
+            y.data_ptr() if want_y else None, cols, qc, ld_c, qs)
     return Normed(q, h, y)
 
 
 def _fp8_workspace(which, M, N, K, ws, dev):
-    """(address, bytes) of the split-K workspace, and the tensor to keep."""
+    """(address, bytes, tensor to keep) of the split-K workspace; sizes that
+    need none get none."""
     if ws is None:
-        ws = _workspace(_native.lib().gptq_workspace_bytes(which, N, K, M, None), dev)
+        need = _native.lib().gptq_workspace_bytes(which, N, K, M, None)
+        if need <= 256:
+            return None, 0, None
+        ws = _workspace(need, dev)
     else:
         _ws_check(ws, dev)
     return ws.data_ptr(), ws.numel(), ws
@@ -664,18 +696,18 @@ def fp8_gemm(A: Fp8Matrix, B: Fp8Matrix, out_dtype=None, out=None, ws=None):
     """C = A·Bᵀ: A [M, K] with block_rows 1, B [N, K] with block_rows 128,
     C [M, N] in out_dtype (bfloat16 unless given, or `out`'s type).
     ws: the split-K workspace (allocated here when None; pass one to reuse)."""
-    torch = _torch()
-    M, K, lda = _fp8_arg(A, "A", 1)
-    dev = A.codes.device
-    N, kb, ldb = _fp8_arg(B, "B", FP8_BLOCK, dev)
+    M, K, lda, dev = _fp8_arg(A, "A", 1)
+    N, kb, ldb, _ = _fp8_arg(B, "B", FP8_BLOCK, dev)
     if kb != K:
         raise ValueError(f"A has {K} columns, B has {kb}")
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype or torch.bfloat16, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out must be {out_dtype} (got {out.dtype})")
-    cdt = _dtype_code(out)
-    ldc = _fp8_out(out, "out", out.dtype, (M, N), dev)
+        out = _t8()[0]((M, N), dtype=out_dtype or _torch().bfloat16, device=dev)
+        ldc = N
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out must be {out_dtype} (got {out.dtype})")
+        ldc = _fp8_out(out, "out", out.dtype, (M, N), dev)
+    cdt = _fp8_dtype(out, "out")
     wp, wn, ws = _fp8_workspace(_native.WS_FP8_GEMM, M, N, K, ws, dev)
     _launch(dev, _native.lib().gptq_fp8_gemm, A.codes.data_ptr(), A.scales.data_ptr(), M, K, lda,
             B.codes.data_ptr(), B.scales.data_ptr(), N, ldb, out.data_ptr(), cdt, ldc, wp, wn)
@@ -692,40 +724,37 @@ def fp8_gated_gemm(A: Fp8Matrix, gate: Fp8Matrix, up: Fp8Matrix, activation: str
     with block_rows 128.  Returns an Fp8Matrix [M, N] with block_rows 1, or a
     tensor of out_dtype where that is given; `out` is either, to be filled.
     ws: the split-K workspace (allocated here when None; pass one to reuse)."""
-    torch = _torch()
-    M, K, lda = _fp8_arg(A, "A", 1)
-    dev = A.codes.device
-    N, kg, ldg = _fp8_arg(gate, "gate", FP8_BLOCK, dev)
-    nu, ku, ldu = _fp8_arg(up, "up", FP8_BLOCK, dev)
+    M, K, lda, dev = _fp8_arg(A, "A", 1)
+    N, kg, ldg, _ = _fp8_arg(gate, "gate", FP8_BLOCK, dev)
+    nu, ku, ldu, _ = _fp8_arg(up, "up", FP8_BLOCK, dev)
     if kg != K or ku != K or nu != N:
         raise ValueError(f"A has {K} columns; gate {(N, kg)} and up {(nu, ku)} do not fit")
-    if activation not in _ACTIVATIONS:
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)} (got {activation!r})")
     cp, cdt, ldc, qc, ldq, qs = None, 0, 0, None, 0, None
-    if out is None:
-        if out_dtype is None:
-            out = Fp8Matrix(_fp8_codes(M, N, dev),
-                            torch.empty(M, (N + FP8_BLOCK - 1) // FP8_BLOCK, dtype=torch.float32,
-                                        device=dev), 1)
-        else:
-            out = torch.empty(M, N, dtype=out_dtype, device=dev)
-    if isinstance(out, Fp8Matrix):
+    if out is None and out_dtype is None:
+        out, ldq = _fp8_new(M, N, 1, dev)
+        qc, qs = out.codes.data_ptr(), out.scales.data_ptr()
+    elif isinstance(out, Fp8Matrix):
         if out_dtype is not None:
             raise ValueError("an Fp8Matrix out has no out_dtype")
-        mo, no, ldq = _fp8_arg(out, "out", 1, dev)
+        mo, no, ldq, _ = _fp8_arg(out, "out", 1, dev)
         if (mo, no) != (M, N):
             raise ValueError(f"out must have shape {(M, N)} (got {(mo, no)})")
         qc, qs = out.codes.data_ptr(), out.scales.data_ptr()
     else:
-        if out_dtype is not None and out.dtype != out_dtype:
+        if out is None:
+            out = _t8()[0]((M, N), dtype=out_dtype, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
             raise ValueError(f"out must be {out_dtype} (got {out.dtype})")
-        cdt = _dtype_code(out)
+        cdt = _fp8_dtype(out, "out")
         ldc = _fp8_out(out, "out", out.dtype, (M, N), dev)
         cp = out.data_ptr()
     wp, wn, ws = _fp8_workspace(_native.WS_FP8_GATED, M, N, K, ws, dev)
     _launch(dev, _native.lib().gptq_fp8_gated_gemm, A.codes.data_ptr(), A.scales.data_ptr(), M, K,
             lda, gate.codes.data_ptr(), gate.scales.data_ptr(), ldg, up.codes.data_ptr(),
-            up.scales.data_ptr(), ldu, N, _ACTIVATIONS[activation], cp, cdt, ldc, qc, ldq, qs, wp, wn)
+            up.scales.data_ptr(), ldu, N, act, cp, cdt, ldc, qc, ldq, qs, wp, wn)
     return out
 
 
