@@ -63,15 +63,23 @@ template <> struct Frag<false> {
     v[2] = up(y[0], y[1]); v[3] = up(y[2], y[3]);
   }
 };
-__device__ __forceinline__ f32x4 contract(const Frag<true>& b, const Frag<true>& a) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,
-                                                          0, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 contract(const Frag<false>& b, const Frag<false>& a) {
-  f32x4 t = {0.f, 0.f, 0.f, 0.f};
+// q[g] = the block's products of b[g] and a
+template <int G>
+__device__ __forceinline__ void contract(const Frag<true>* b, const Frag<true>& a, f32x4 (&q)[G]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[i], a.v[i], t, 0, 0, 0);
-  return t;
+  for (int g = 0; g < G; ++g)
+    q[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[g].v, a.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0,
+                                                            0, 0, 0, 0, 0);
+}
+template <int G>
+__device__ __forceinline__ void contract(const Frag<false>* b, const Frag<false>& a, f32x4 (&q)[G]) {
+#pragma unroll
+  for (int g = 0; g < G; ++g) q[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      q[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[g].v[i], a.v[i], q[g], 0, 0, 0);
 }
 
 // 16 bytes of a row from byte k on; bytes past the row's K and rows that do
@@ -142,9 +150,7 @@ template <int BM, int BN, int WM, int WN, int NS> struct Tile {
   static constexpr int SMEM = SCALES + 2 * SCB;
   static constexpr int SCOPIES = BM / 8 + 1;            // copies of eight blocks' scales
   static_assert(SEGS % WAVES == 0 && NS >= 2 && NS <= 4, "copy plan");
-  // issued over the stages of the eight blocks before, the last of them early
-  // enough for the stage barriers to cover them
-  static_assert(SCOPIES <= (8 - NS + 1) * WAVES && (NS - 2) * PER <= 63, "copy plan");
+  static_assert((NS - 2) * PER <= 63, "vmcnt range");
 };
 
 // Waits until all copies but the last `ahead` stages' (loads complete in issue
@@ -174,6 +180,9 @@ template <int BM, int BN, int WM, int WN, int NS, bool FAST, bool GATED, int EPI
 __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel(GArgs a) {
   using T = Tile<BM, BN, WM, WN, NS>;
   constexpr int MI = T::MI, NI = T::NI, NB = GATED ? 2 : 1;
+  // B pieces a step takes: the exact form's four instructions depend on each
+  // other, so two pieces run side by side where registers allow
+  constexpr int G = !FAST && MI * NI < 32 ? 2 : 1;
   constexpr int BC = BN / NB;      // columns of C
   constexpr int WC = WN / NB;      // ... of a wave
   __shared__ __attribute__((aligned(1024))) char S[T::SMEM];
@@ -202,39 +211,44 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
     const int half = GATED && seg >= (BM + BC) / 8;
     return (int64_t)min(row - BM - half * BC, nleft - 1) * a.ldb[half] + p16;
   };
-  // The exact form has no registers left to keep its offsets in (a spill
-  // would wait for the copies in flight) and computes them anew each stage.
-  uint32_t voff[FAST ? T::PER : 1];
-  if constexpr (FAST) {
+  // The exact form with the largest tile has no registers left to keep its
+  // offsets in (a spill would wait for the copies in flight) and computes them
+  // anew each stage.
+  constexpr bool KEEP = FAST || MI * NI < 32;
+  uint32_t voff[KEEP ? T::PER : 1];
+  if constexpr (KEEP) {
 #pragma unroll
     for (int i = 0; i < T::PER; ++i) voff[i] = (uint32_t)seg_offset(w * T::PER + i, lane);
   }
   const unsigned sbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)S;
   const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;   // blocks from here on: bytewise
-  // copy `idx` of the scales of blocks 8·g.. of this split
-  auto copy_scales = [&](int g, int idx) {
+  // the wave's copies of the scales of blocks 8·g.. of this split
+  auto copy_scales = [&](int g) {
     int l = lane;
-    if constexpr (!FAST) asm volatile("" : "+v"(l));   // not hoisted
+    asm volatile("" : "+v"(l));   // eight stages apart: not worth registers
     const int r = l >> 3, k = min(kbeg + 8 * g + (l & 7), a.kb - 1);
-    const float* p;
-    if (idx < BM / 8) p = a.sa + (m0 + min(idx * 8 + r, mleft - 1)) * a.kb;
-    else if (GATED) p = (r == 0 ? a.sb[0] : a.sb[NB - 1]) + n0 / 128 * a.kb;
-    else p = a.sb[0] + min(n0 / 128 + min(r, 1), a.nb - 1) * a.kb;
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
-                 :: "s"(sbase + T::SCALES + (unsigned)((g & 1) * T::SCB + idx * 256)), "v"(p + k) : "memory");
+#pragma unroll
+    for (int idx = w; idx < T::SCOPIES; idx += T::WAVES) {
+      const float* p;
+      if (idx < BM / 8) p = a.sa + (m0 + min(idx * 8 + r, mleft - 1)) * a.kb;
+      else if (GATED) p = (r == 0 ? a.sb[0] : a.sb[NB - 1]) + n0 / 128 * a.kb;
+      else p = a.sb[0] + min(n0 / 128 + min(r, 1), a.nb - 1) * a.kb;
+      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
+                   :: "s"(sbase + T::SCALES + (unsigned)((g & 1) * T::SCB + idx * 256)), "v"(p + k) : "memory");
+    }
   };
   auto copy = [&](int st) {
     const unsigned buf = (unsigned)((st % NS) * T::SB);
     if (kbeg + st < last_wide) {
       int l = lane;
-      if constexpr (!FAST) asm volatile("" : "+v"(l));   // not hoisted
+      if constexpr (!KEEP) asm volatile("" : "+v"(l));   // not hoisted
 #pragma unroll
       for (int i = 0; i < T::PER; ++i) {
         const int seg = w * T::PER + i;
         // 16 bytes per lane to LDS M0 + 16·lane; no register result, ordered
         // before the reads by the stage barriers
         asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
-                     :: "s"(sbase + buf + (unsigned)seg * 1024u), "v"(FAST ? voff[FAST ? i : 0] : (uint32_t)seg_offset(seg, l)),
+                     :: "s"(sbase + buf + (unsigned)seg * 1024u), "v"(KEEP ? voff[KEEP ? i : 0] : (uint32_t)seg_offset(seg, l)),
                         "s"(seg_base(seg) + (int64_t)(kbeg + st) * 128)
                      : "memory");
       }
@@ -277,7 +291,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
   };
 
   if (nst > 0) {
-    for (int i = w; i < T::SCOPIES; i += T::WAVES) copy_scales(0, i);
+    copy_scales(0);
     for (int s0 = 0; s0 < NS - 1 && s0 < nst; ++s0) copy(s0);
     stage_barrier<T::PER>(min(nst - 1, NS - 2));
     // The loop is software-pipelined by hand: step (i, j) multiplies A piece i
@@ -296,16 +310,13 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
     for (int q = 0; q < NB; ++q) sb[q] = *reinterpret_cast<const float*>(S + boff + 32 * q);
     for (int st = 0; st < nst; ++st) {
       if (st + NS - 1 < nst) copy(st + NS - 1);
-      {
-        const int i = (st & 7) * T::WAVES + w;
-        if (i < T::SCOPIES && (st | 7) + 1 < nst) copy_scales((st >> 3) + 1, i);
-      }
+      if ((st & 7) == 0 && st + 8 < nst) copy_scales((st >> 3) + 1);
       const char* sc = scales_of(st);
       const char* sc_ = scales_of(st + 1);
       const char* b = S + (st % NS) * T::SB;
       const char* bn_ = S + ((st + 1) % NS) * T::SB;
-      f32x4 p;
-      float sp = 0.f, s[NB];
+      f32x4 p[G];
+      float sp[G] = {}, s[NB];
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         fa.set(ra.x, ra.y);
@@ -320,14 +331,21 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-          f32x4 q = contract(fb[j], fa);
-          // keeps the adds below behind this product
-          if (i + j > 0) asm volatile("" : "+v"(q), "+v"(p));
-          else asm volatile("" : "+v"(q));
+        for (int j = 0; j < NI; j += G) {
+          f32x4 q[G];
+          contract(&fb[j], fa, q);
+          // keeps the adds below behind these products
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            if (i + j > 0) asm volatile("" : "+v"(q[g]), "+v"(p[g]));
+            else asm volatile("" : "+v"(q[g]));
+          }
           if (i + 1 == MI) {   // the next stage's pieces (past the last stage: unused bytes)
-            const Raw r = read_b(bn_, j);
-            fb[j].set(r.x, r.y);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const Raw r = read_b(bn_, j + g);
+              fb[j + g].set(r.x, r.y);
+            }
             if (j == 0) {
               ra = read_a(bn_, 0);
               sn = *reinterpret_cast<const float*>(sc_ + soff);
@@ -335,20 +353,29 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
               for (int h = 0; h < NB; ++h) sb[h] = *reinterpret_cast<const float*>(sc_ + boff + 32 * h);
             }
           }
-          const int pi = j > 0 ? i : i - 1, pj = j > 0 ? j - 1 : NI - 1;
+          const int pi = j > 0 ? i : i - 1, pj = j > 0 ? j - G : NI - G;
           if (pi >= 0) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[pj][pi][r] = __builtin_fmaf(p[r], sp, acc[pj][pi][r]);
-            asm volatile("" : "+v"(acc[pj][pi]));   // ... and here
+            for (int g = 0; g < G; ++g) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                acc[pj + g][pi][r] = __builtin_fmaf(p[g][r], sp[g], acc[pj + g][pi][r]);
+              asm volatile("" : "+v"(acc[pj + g][pi]));   // ... and here
+            }
           }
-          p = q;
-          sp = s[GATED ? j / (NI / 2) : 0];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            p[g] = q[g];
+            sp[g] = s[GATED ? (j + g) / (NI / 2) : 0];
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        acc[NI - 1][MI - 1][r] = __builtin_fmaf(p[r], sp, acc[NI - 1][MI - 1][r]);
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[NI - G + g][MI - 1][r] = __builtin_fmaf(p[g][r], sp[g], acc[NI - G + g][MI - 1][r]);
     }
     __syncthreads();   // the epilogue reuses the stage buffers
   }
@@ -501,9 +528,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GArgs a) {
       for (int b = 0; b < NB; ++b) {
         Frag<FAST> fb;
         fb.set(rb[d][b][0], rb[d][b][1]);
-        const f32x4 p = contract(fb, fa);
+        f32x4 p[1];
+        contract(&fb, fa, p);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[b][r] = __builtin_fmaf(p[r], s[d][b], acc[b][r]);
+        for (int r = 0; r < 4; ++r) acc[b][r] = __builtin_fmaf(p[0][r], s[d][b], acc[b][r]);
       }
       load(d, kb + D * kFewWaves);
     }
