@@ -182,7 +182,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
   constexpr int MI = T::MI, NI = T::NI, NB = GATED ? 2 : 1;
   // B pieces a step takes: the exact form's four instructions depend on each
   // other, so two pieces run side by side where registers allow
-  constexpr int G = !FAST && MI * NI < 32 ? 2 : 1;
+  constexpr int G = !FAST && MI * NI < 32 && NI % 2 == 0 ? 2 : 1;
   constexpr int BC = BN / NB;      // columns of C
   constexpr int WC = WN / NB;      // ... of a wave
   __shared__ __attribute__((aligned(1024))) char S[T::SMEM];
@@ -382,6 +382,21 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
 
   const int nl = wn * WC + 4 * (lane >> 4);   // this lane's first column in the tile
   if constexpr (EPI == kPartial) {
+    if (GATED && a.kper >= a.kb) {   // unsplit: h itself
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int ml = wm * WM + i * 16 + l15;
+#pragma unroll
+        for (int j = 0; j < NI / NB; ++j) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[j][i][r] = activate(acc[j][i][r], a.act) * acc[NI / NB + j][i][r];
+          if (ml < mleft)
+            put4<GPTQ_F32>(a.P, (m0 + ml) * a.N + n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+        }
+      }
+      return;
+    }
     float* P = a.P + (int64_t)split * NB * a.M * a.N;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -461,105 +476,128 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
 }
 
 // ---------------------------------------------------------------- few rows
-// Up to 16 rows of A: the weights' bytes are what counts.  A workgroup owns
-// 16 columns (of gate and up for GATED) and its eight waves every eighth
-// block of K; operands go from memory straight into registers, each weight
-// byte once, D blocks in flight; the waves' sums are added in wave order.
-constexpr int kFewRows = 16, kFewWaves = 8;
+// Up to 48 rows of A (MT pieces of 16): the weights' bytes are what counts.  A
+// workgroup owns 16 columns (of gate and up for GATED) and its eight waves
+// every eighth block of K; operands go from memory straight into registers,
+// each weight byte once, D blocks ahead, with no barrier in the loop; the
+// waves' sums are added in wave order.
+constexpr int kFewRows = 48, kFewWaves = 8;
 
-template <bool FAST, bool GATED, int EPI>
+template <int MT, bool FAST, bool GATED, int EPI>
 __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GArgs a) {
-  constexpr int NB = GATED ? 2 : 1, D = GATED ? 2 : 4;
-  __shared__ float part[kFewWaves][NB][16][17];
+  constexpr int NB = GATED ? 2 : 1, D = MT == 1 ? 3 : 2;
+  __shared__ float part[kFewWaves][NB][MT * 16][17];
   const int t = threadIdx.x, lane = t & 63, l15 = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const bool mok = l15 < a.M, nok = n0 + l15 < a.N;
-  const int64_t blk = n0 / 128;
   const int kp = 16 * (lane >> 4);
-  const uint8_t* ap = a.A + (mok ? l15 : 0) * a.lda;
-  const uint8_t* bp[NB];
+  const uint8_t *ap[MT], *bp[NB];
+  const float *sap[MT], *sbp[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) bp[b] = a.B[b] + (nok ? n0 + l15 : a.N - 1) * a.ldb[b];
-  const float* sap = a.sa + (mok ? l15 : 0) * (int64_t)a.kb;
-  f32x4 acc[NB];
+  for (int i = 0; i < MT; ++i) {   // rows that do not exist: row 0, never stored
+    const int64_t m = i * 16 + l15 < a.M ? i * 16 + l15 : 0;
+    ap[i] = a.A + m * a.lda + kp;
+    sap[i] = a.sa + m * a.kb;
+  }
 #pragma unroll
-  for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int b = 0; b < NB; ++b) {
+    bp[b] = a.B[b] + min(n0 + l15, a.N - 1) * a.ldb[b] + kp;
+    sbp[b] = a.sb[b] + n0 / 128 * a.kb;
+  }
+  f32x4 acc[NB][MT];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  i32x4 ra[D][2], rb[D][NB][2];
-  float s[D][NB];
+  struct Raw { i32x4 x, y; };
+  Raw ra[D][MT], rb[D][NB];
+  float sa[D][MT], sb[D][NB];
   const int full = (int)(a.K / 128);   // whole blocks
   auto load = [&](int d, int kb) {
+    const int64_t k = (int64_t)kb * 128;
     if (kb < full) {
-      const int64_t k = (int64_t)kb * 128 + kp;
-      __builtin_memcpy(&ra[d][0], ap + k, 16);
-      __builtin_memcpy(&ra[d][1], ap + k + 64, 16);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        __builtin_memcpy(&rb[d][b][0], bp[b] + k, 16);
-        __builtin_memcpy(&rb[d][b][1], bp[b] + k + 64, 16);
+        __builtin_memcpy(&rb[d][b].x, bp[b] + k, 16);
+        __builtin_memcpy(&rb[d][b].y, bp[b] + k + 64, 16);
       }
-    } else if (kb < a.kb) {
-      const int64_t k = (int64_t)kb * 128 + kp;
-      ra[d][0] = piece16(ap, k, a.K, true);
-      ra[d][1] = piece16(ap, k + 64, a.K, true);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        __builtin_memcpy(&ra[d][i].x, ap[i] + k, 16);
+        __builtin_memcpy(&ra[d][i].y, ap[i] + k + 64, 16);
+      }
+    } else {   // the rows end inside this block
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        rb[d][b][0] = piece16(bp[b], k, a.K, true);
-        rb[d][b][1] = piece16(bp[b], k + 64, a.K, true);
+        rb[d][b].x = piece16(bp[b] - kp, k + kp, a.K, true);
+        rb[d][b].y = piece16(bp[b] - kp, k + kp + 64, a.K, true);
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        ra[d][i].x = piece16(ap[i] - kp, k + kp, a.K, true);
+        ra[d][i].y = piece16(ap[i] - kp, k + kp + 64, a.K, true);
       }
     }
-    if (kb < a.kb) {
-      const float x = sap[kb];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) s[d][b] = x * a.sb[b][blk * a.kb + kb];
-    }
+    for (int b = 0; b < NB; ++b) sb[d][b] = sbp[b][kb];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sa[d][i] = sap[i][kb];
   };
 #pragma unroll
-  for (int d = 0; d < D; ++d) load(d, w + d * kFewWaves);
+  for (int d = 0; d < D; ++d)
+    if (w + d * kFewWaves < a.kb) load(d, w + d * kFewWaves);
   for (int k0 = w; k0 < a.kb; k0 += D * kFewWaves) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       const int kb = k0 + d * kFewWaves;
       if (kb >= a.kb) break;
-      Frag<FAST> fa;
-      fa.set(ra[d][0], ra[d][1]);
+      Frag<FAST> fb[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        Frag<FAST> fb;
-        fb.set(rb[d][b][0], rb[d][b][1]);
-        f32x4 p[1];
-        contract(&fb, fa, p);
+      for (int b = 0; b < NB; ++b) fb[b].set(rb[d][b].x, rb[d][b].y);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[b][r] = __builtin_fmaf(p[0][r], s[d][b], acc[b][r]);
+      for (int i = 0; i < MT; ++i) {
+        Frag<FAST> fa;
+        fa.set(ra[d][i].x, ra[d][i].y);
+        f32x4 p[NB];
+        contract(fb, fa, p);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float s = sa[d][i] * sb[d][b];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[b][i][r] = __builtin_fmaf(p[b][r], s, acc[b][i][r]);
+        }
       }
-      load(d, kb + D * kFewWaves);
+      if (kb + D * kFewWaves < a.kb) load(d, kb + D * kFewWaves);
     }
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) part[w][b][l15][4 * (lane >> 4) + r] = acc[b][r];
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[w][b][i * 16 + l15][4 * (lane >> 4) + r] = acc[b][i][r];
   __syncthreads();
-  if (t >= 256) return;
-  const int m = t >> 4, c = t & 15;
+  const int c = t & 15;
   const int64_t n = n0 + c;
-  if (m >= a.M || n >= a.N) return;
-  float h[NB];
+  if (n >= a.N) return;
+  for (int m = t >> 4; m < MT * 16 && m < a.M; m += kFewWaves * 4) {
+    float h[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    h[b] = 0.f;
+    for (int b = 0; b < NB; ++b) {
+      h[b] = 0.f;
 #pragma unroll
-    for (int q = 0; q < kFewWaves; ++q) h[b] += part[q][b][m][c];
-  }
-  float x = h[0];
-  if constexpr (GATED) x = activate(h[0], a.act) * h[NB - 1];
-  if constexpr (EPI == kPartial) {
-    a.P[(int64_t)m * a.N + n] = x;     // h itself: one partial, activated
-  } else {
-    if (a.c_dt == GPTQ_F32) static_cast<float*>(a.C)[m * a.ldc + n] = x;
-    else if (a.c_dt == GPTQ_BF16) static_cast<__bf16*>(a.C)[m * a.ldc + n] = (__bf16)x;
-    else static_cast<_Float16*>(a.C)[m * a.ldc + n] = (_Float16)x;
+      for (int q = 0; q < kFewWaves; ++q) h[b] += part[q][b][m][c];
+    }
+    float x = h[0];
+    if constexpr (GATED) x = activate(h[0], a.act) * h[NB - 1];
+    if constexpr (EPI == kPartial) {
+      a.P[(int64_t)m * a.N + n] = x;     // h itself: one partial, activated
+    } else {
+      if (a.c_dt == GPTQ_F32) static_cast<float*>(a.C)[m * a.ldc + n] = x;
+      else if (a.c_dt == GPTQ_BF16) static_cast<__bf16*>(a.C)[m * a.ldc + n] = (__bf16)x;
+      else static_cast<_Float16*>(a.C)[m * a.ldc + n] = (_Float16)x;
+    }
   }
 }
 
@@ -612,28 +650,68 @@ __global__ __launch_bounds__(256) void join_kernel(GArgs a, int splits) {
 }
 
 // ---------------------------------------------------------------- choice and launch
-struct Plan { int bm, bc; int splits, kper; bool few; };
+// The kernel for a product is the one that this model says is quickest.  Its
+// times are microseconds measured on MI355X at K = 4096 (fp8 instructions /
+// exact form): a stage of a tile with one workgroup on each of the 256 CUs,
+// and with as many as fit; launches with more take proportionally longer.
+// Small tiles win where there are few (512 x 4096: 64-tiles 18.7 / 29.1 us,
+// 128-tiles in two splits 25.2 / 31.3, 256-tiles in eight 39 / 45), large ones
+// where there are many (4096 x 4096: 131 / 201, 83 / 140, 67 / 118).
+struct TileCost { int bm, bn, fit; double one[2], full[2]; };   // [0] fp8, [1] exact
+constexpr TileCost kTiles[] = {
+    {32, 64, 3, {0.25, 0.45}, {0.50, 0.85}},
+    {64, 64, 2, {0.35, 0.62}, {0.46, 0.78}},
+    {128, 128, 2, {0.79, 1.16}, {1.20, 2.11}},
+    {256, 256, 1, {1.98, 3.57}, {1.98, 3.57}},
+};
+constexpr int kTileKinds = 4;
+constexpr double kLaunch = 4.0, kJoin = 3.5, kJoinBytes = 4.5e6;   // us, us, bytes per us
+constexpr double kFewLaunch = 2.5, kFewCopies = 7.0e3;             // us, KB of operands per us
 
-Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool ws) {
-  Plan p{};
-  const int kb = (int)ceil_div(K, 128);
-  p.few = M <= kFewRows;
-  p.splits = 1;
-  p.kper = kb;
-  if (p.few) return p;
-  const int64_t big = ceil_div(M, 256) * ceil_div(N, gated ? 128 : 256);
-  const bool large = big >= 192;
-  p.bm = large ? 256 : 128;
-  p.bc = large ? (gated ? 128 : 256) : 128;
-  if (ws && !large) {
-    const int64_t tiles = ceil_div(M, p.bm) * ceil_div(N, p.bc);
-    const int64_t s = std::min<int64_t>(std::min<int64_t>(ceil_div(256, tiles), 16), kb / 2);
-    if (s > 1) {
-      p.kper = (int)ceil_div(kb, s);
-      p.splits = (int)ceil_div(kb, p.kper);
+struct Plan { int tile; int splits, kper; };   // tile -1: few rows
+
+// join: the result goes through the workspace in any case (codes of a tile
+// that is not a block wide).  Without a workspace one split of the 256-tile
+// runs for codes, any unsplit kernel otherwise.
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool exact, bool codes, bool ws) {
+  const int nb = gated ? 2 : 1, e = exact ? 1 : 0;
+  const int64_t kb = ceil_div(K, 128);
+  Plan best{kTileKinds - 1, 1, (int)kb};
+  double least = 1e300;
+  if (M <= kFewRows && (!codes || ws)) {
+    const double mt = (double)ceil_div(M, 16);
+    // a piece with few real rows hits the first-level cache
+    const double kbytes = (double)ceil_div(N, 16) * kb * 2 * (nb + mt * std::min<double>(1.0, M / 12.0));
+    least = kFewLaunch + kbytes / kFewCopies + (codes ? kJoin : 0);
+    best = {-1, 1, (int)kb};
+  }
+  for (int i = 0; i < kTileKinds; ++i) {
+    const TileCost& c = kTiles[i];
+    const bool join = codes && c.bn < 256;
+    if (join && !ws) continue;
+    const int64_t tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn / nb);
+    for (int64_t s = 1; s <= 16 && s <= std::max<int64_t>(1, kb / 2); ++s) {
+      if (s > 1 && (!ws || tiles * s > 1024)) break;
+      const int64_t kper = ceil_div(kb, s);
+      if (s > 1 && ceil_div(kb, kper) != s) continue;
+      const double load = (double)ceil_div(tiles * s, 256);
+      const double stage = load <= 1 ? c.one[e]
+                           : load < c.fit ? c.one[e] + (c.full[e] - c.one[e]) * (load - 1) / (c.fit - 1)
+                                          : c.full[e] * load / c.fit;
+      double t = kLaunch + stage * kper;
+      if (s > 1 || join) t += kJoin + (double)(s > 1 ? s * nb : 1) * M * N * 8 / kJoinBytes;
+      if (t < least) {
+        least = t;
+        best = {i, (int)s, (int)kper};
+      }
     }
   }
-  return p;
+  return best;
+}
+
+size_t plan_bytes(const Plan& p, int64_t M, int64_t N, bool gated, bool codes) {
+  if (p.splits > 1) return (size_t)p.splits * (gated ? 2 : 1) * M * N * 4;
+  return codes && p.tile != kTileKinds - 1 ? (size_t)M * N * 4 : 0;
 }
 
 template <int BM, int BN, int WM, int WN, int NS, bool FAST, bool GATED, int EPI, int DT>
@@ -647,11 +725,29 @@ hipError_t launch_tile(GArgs& a, int splits, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <bool FAST, bool GATED, int EPI, int DT>
+hipError_t launch_kind(GArgs& a, const Plan& p, hipStream_t s) {
+  switch (p.tile) {
+    case 0: return launch_tile<32, 64, 16, 32, 4, FAST, GATED, EPI, DT>(a, p.splits, s);
+    case 1: return launch_tile<64, 64, 32, 32, 4, FAST, GATED, EPI, DT>(a, p.splits, s);
+    case 2: return launch_tile<128, 128, 64, 32, 2, FAST, GATED, EPI, DT>(a, p.splits, s);
+    default: return launch_tile<256, 256, 128, 64, 2, FAST, GATED, EPI, DT>(a, p.splits, s);
+  }
+}
+
+template <bool FAST, bool GATED, int EPI> hipError_t launch_few(const GArgs& a, hipStream_t s) {
+  const unsigned grid = (unsigned)ceil_div(a.N, 16), nt = kFewWaves * 64;
+  if (a.M <= 16) few_rows_kernel<1, FAST, GATED, EPI><<<grid, nt, 0, s>>>(a);
+  else if (a.M <= 32) few_rows_kernel<2, FAST, GATED, EPI><<<grid, nt, 0, s>>>(a);
+  else few_rows_kernel<3, FAST, GATED, EPI><<<grid, nt, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 // One output form: EPI with DT (FAST goes with the 16-bit types).
 template <bool GATED, int EPI, int DT>
 hipError_t run(GArgs& a, void* ws, hipStream_t s) {
-  constexpr bool FAST = EPI == kStore && DT != GPTQ_F32;
-  const Plan p = plan_of(a.M, a.N, a.K, GATED, ws != nullptr);
+  constexpr bool FAST = EPI == kStore && DT != GPTQ_F32, codes = EPI == kCodes;
+  const Plan p = plan_of(a.M, a.N, a.K, GATED, !FAST, codes, ws != nullptr);
   a.nb = ceil_div(a.N, 128);
   a.kb = (int)ceil_div(a.K, 128);
   a.kper = p.kper;
@@ -661,27 +757,17 @@ hipError_t run(GArgs& a, void* ws, hipStream_t s) {
     return (uintptr_t)q % 16 == 0 && (rows == 1 || (ld % 16 == 0 && ld < ((int64_t)1 << 23)));
   };
   a.wide = wide(a.A, a.M, a.lda) && wide(a.B[0], a.N, a.ldb[0]) && (!GATED || wide(a.B[1], a.N, a.ldb[1]));
-  constexpr bool codes = EPI == kCodes;
+  const bool join = p.splits > 1 || (codes && p.tile != kTileKinds - 1);
   hipError_t e;
-  if (p.few && !(codes && !ws)) {
-    const unsigned grid = (unsigned)ceil_div(a.N, 16);
-    if (!codes) {
-      few_rows_kernel<FAST, GATED, kStore><<<grid, kFewWaves * 64, 0, s>>>(a);
-      return hipGetLastError();
-    }
-    few_rows_kernel<FAST, GATED, kPartial><<<grid, kFewWaves * 64, 0, s>>>(a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    join_kernel<false, true><<<(unsigned)ceil_div(a.M * a.nb, 16), 256, 0, s>>>(a, 1);
-    return hipGetLastError();
-  }
-  if (p.splits > 1) {
-    e = launch_tile<128, GATED ? 256 : 128, 64, 64, 2, FAST, GATED, kPartial, GPTQ_F32>(a, p.splits, s);
-    if (e != hipSuccess) return e;
-    join_kernel<GATED, codes><<<(unsigned)ceil_div(a.M * a.nb, 16), 256, 0, s>>>(a, p.splits);
-    return hipGetLastError();
-  }
-  if (p.bm == 256) return launch_tile<256, 256, 128, 64, 2, FAST, GATED, EPI, DT>(a, 1, s);
-  return launch_tile<128, GATED ? 256 : 128, 64, 64, 2, FAST, GATED, EPI, DT>(a, 1, s);
+  if (p.tile < 0) e = launch_few<FAST, GATED, codes ? kPartial : kStore>(a, s);
+  else if (join) e = launch_kind<FAST, GATED, kPartial, GPTQ_F32>(a, p, s);
+  else if constexpr (codes) e = launch_tile<256, 256, 128, 64, 2, false, true, kCodes, DT>(a, 1, s);
+  else e = launch_kind<FAST, GATED, EPI, DT>(a, p, s);
+  if (e != hipSuccess || !join) return e;
+  const unsigned grid = (unsigned)ceil_div(a.M * a.nb, 16);
+  if (p.splits > 1) join_kernel<GATED, codes><<<grid, 256, 0, s>>>(a, p.splits);
+  else join_kernel<false, codes><<<grid, 256, 0, s>>>(a, 1);   // h itself
+  return hipGetLastError();
 }
 
 template <bool GATED> hipError_t run_dt(GArgs& a, void* ws, hipStream_t s) {
@@ -694,10 +780,14 @@ template <bool GATED> hipError_t run_dt(GArgs& a, void* ws, hipStream_t s) {
   }
 }
 
+// enough for every output form
 size_t ws_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
-  const Plan p = plan_of(M, N, K, gated, true);
-  if (p.few) return gated ? align_up((size_t)M * N * 4) : 256;
-  return p.splits > 1 ? align_up((size_t)p.splits * (gated ? 2 : 1) * M * N * 4) : 256;
+  size_t most = 256;
+  for (int form = 0; form < (gated ? 3 : 2); ++form) {   // 16 bits, fp32, codes
+    const Plan p = plan_of(M, N, K, gated, form > 0, form == 2, true);
+    most = std::max(most, plan_bytes(p, M, N, gated, form == 2));
+  }
+  return align_up(most);
 }
 
 }  // namespace
