@@ -696,19 +696,18 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool exact, bool codes
     const bool join = codes && c.bn < 256;
     if (join && !ws) continue;
     const int64_t tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn / nb);
-    for (int64_t s = 1; s <= 16 && s <= std::max<int64_t>(1, kb / 2); ++s) {
-      if (s > 1 && (!ws || tiles * s > 1024)) break;
-      const int64_t kper = ceil_div(kb, s);
-      if (s > 1 && ceil_div(kb, kper) != s) continue;
-      const double load = (double)ceil_div(tiles * s, 256);
+    for (const int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (s > 1 && (!ws || tiles * s > 1024 || 2 * s > kb)) break;
+      const int kper = ((int)kb + s - 1) / s, splits = ((int)kb + kper - 1) / kper;
+      const int64_t load = (tiles * splits + 255) >> 8;   // workgroups of a CU
       const double stage = load <= 1 ? c.one[e]
                            : load < c.fit ? c.one[e] + (c.full[e] - c.one[e]) * (load - 1) / (c.fit - 1)
                                           : c.full[e] * load / c.fit;
       double t = kLaunch + stage * kper;
-      if (s > 1 || join) t += kJoin + (double)(s > 1 ? s * nb : 1) * M * N * 8 / kJoinBytes;
+      if (s > 1 || join) t += kJoin + (double)(s > 1 ? splits * nb : 1) * M * N * 8 / kJoinBytes;
       if (t < least) {
         least = t;
-        best = {i, (int)s, (int)kper};
+        best = {i, splits, kper};
       }
     }
   }
