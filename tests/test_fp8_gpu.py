@@ -217,12 +217,19 @@ SHAPES = [(1, 1, 1), (1, 128, 128), (1, 4096, 4096), (2, 100, 300), (3, 1000, 10
           (1000, 2100, 256), (2048, 2304, 896), (2100, 6300, 300), (2000, 7000, 640)]
 
 
-@pytest.mark.parametrize("i,shape", list(enumerate(SHAPES)))
-def test_gemm(i, shape):
-    """Every size with and without a workspace; the three output types in turn."""
+# every kernel the sizes choose between, split and unsplit
+SHAPES = [(*s, ["f32", "bf16", "f16"][i % 3]) for i, s in enumerate(SHAPES)] + [
+    (54, 122, 204, "bf16"), (51, 126, 2303, "f16"), (50, 122, 1384, "f32"), (229, 129, 5362, "bf16"),
+    (480, 129, 1958, "f32"), (385, 7173, 211, "bf16"), (301, 6540, 200, "f32"), (66, 2803, 6309, "f16"),
+    (65, 1350, 5633, "f32"), (1951, 6168, 203, "f16"), (131, 5510, 7906, "f32"), (3216, 1423, 7218, "bf16"),
+    (20, 17000, 300, "bf16"), (47, 2000, 640, "bf16"), (16, 130, 65536, "bf16"), (49, 130, 65530, "f32")]
+
+
+@pytest.mark.parametrize("M,N,K,dtype", SHAPES)
+def test_gemm(M, N, K, dtype):
+    """Every size with and without a workspace, and twice the same."""
     torch = torch_mod()
-    M, N, K = shape
-    dtype = ["f32", "bf16", "f16"][i % 3]
+    shape = (M, N, K)
     a, b = _matrix(M, K, 1, 1), _matrix(N, K, 128, 2, 0.05)
     ref, mag = fp8.matmul(_values(a), _values(b))
     bound = fp8.accumulation_bound(mag, K, grouped=dtype != "f32")
@@ -245,10 +252,18 @@ GATED = [(1, 1, 1, "silu"), (1, 4096, 1024, "silu"), (4, 1000, 4096, "gelu"), (9
          (2100, 3200, 300, "silu"), (1800, 4100, 256, "gelu_tanh")]
 
 
-@pytest.mark.parametrize("i,shape", list(enumerate(GATED)))
-def test_gated(i, shape):
+GATED = [(*s, ["f32", "bf16", "f16"][i % 3]) for i, s in enumerate(GATED)] + [
+    (51, 126, 2303, "silu", "bf16"), (50, 122, 1384, "gelu", "f32"), (65, 2823, 202, "silu", "f16"),
+    (67, 231, 5226, "silu", "bf16"), (66, 464, 1924, "gelu_tanh", "f32"), (213, 6510, 200, "silu", "bf16"),
+    (165, 5605, 207, "silu", "f32"), (65, 3284, 5935, "silu", "f16"), (67, 1421, 3204, "silu", "f32"),
+    (1282, 4452, 203, "silu", "bf16"), (135, 2942, 7038, "gelu", "f32"), (456, 4178, 6348, "silu", "bf16"),
+    (20, 9000, 300, "gelu", "bf16")]
+
+
+@pytest.mark.parametrize("M,N,K,act,dtype", GATED)
+def test_gated(M, N, K, act, dtype):
     torch = torch_mod()
-    M, N, K, act = shape
+    shape = (M, N, K, act)
     a, g_, u = _matrix(M, K, 1, 1), _matrix(N, K, 128, 2, 0.05), _matrix(N, K, 128, 3, 0.05)
     ref, bound = fp8.gated(_values(a), _values(g_), _values(u), act)
     n = gq()._native
@@ -263,7 +278,6 @@ def test_gated(i, shape):
             torch.cuda.current_stream().cuda_stream)
         assert rc == n.OK, n.last_error()
 
-    dtype = ["f32", "bf16", "f16"][i % 3]
     wide = fp8.gated(_values(a), _values(g_), _values(u), act, grouped=dtype != "f32")[1]
     C = gq().fp8_gated_gemm(a, g_, u, act, out_dtype=_t(dtype))
     _check(C, ref, wide, dtype, f"GATED {shape} {dtype}")
@@ -397,6 +411,45 @@ def test_feed_forward_block_in_a_graph_and_on_a_stream():
             assert torch.equal(h, want[i][0]) and torch.equal(C, want[i][2])
             assert np.array_equal(_codes(q), _codes(want[i][1])) and torch.equal(q.scales, want[i][1].scales)
             assert torch.equal(eager[2], want[(i + 1) % 4][2])
+
+
+def test_two_streams_at_once():
+    """Split products on two streams, each with its own workspace, in turn
+    and at once: the same bits."""
+    torch = torch_mod()
+    a, b, u = _matrix(100, 4096, 1, 1), _matrix(700, 4096, 128, 2, 0.05), _matrix(700, 4096, 128, 3, 0.05)
+    want, wq = gq().fp8_gemm(a, b), gq().fp8_gated_gemm(a, b, u)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in (s, t):
+        st.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(20):
+        with torch.cuda.stream(s):
+            got.append((gq().fp8_gemm(a, b), want))
+        with torch.cuda.stream(t):
+            got.append((gq().fp8_gated_gemm(a, b, u), wq))
+    torch.cuda.synchronize()
+    for x, y in got:
+        if isinstance(x, torch.Tensor):
+            assert torch.equal(x, y)
+        else:
+            assert torch.equal(x.scales, y.scales) and np.array_equal(_codes(x), _codes(y))
+
+
+def test_a_workspace_of_ones_own_is_used_and_checked():
+    torch = torch_mod()
+    n = gq()._native
+    a, b = _matrix(100, 4096, 1, 1), _matrix(700, 4096, 128, 2, 0.05)
+    need = n.lib().gptq_workspace_bytes(n.WS_FP8_GEMM, 700, 4096, 100, None)
+    assert need > 256
+    ws = torch.full((need + 256,), 0x7F, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        assert torch.equal(gq().fp8_gemm(a, b, ws=ws[:need]), gq().fp8_gemm(a, b))
+    assert torch.all(ws[need:] == 0x7F)
+    with pytest.raises(gq().GPTQError):
+        gq().fp8_gemm(a, b, ws=ws[:need - 256])
+    with pytest.raises(ValueError):
+        gq().fp8_gemm(a, b, ws=ws.cpu())
 
 
 def test_gptq_weights_into_the_8_bit_product():
