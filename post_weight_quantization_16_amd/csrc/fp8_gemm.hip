@@ -482,127 +482,168 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
 }
 
 // ---------------------------------------------------------------- few rows
-// Up to 48 rows of A (MT pieces of 16): the weights' bytes are what counts.  A
-// workgroup owns 16 columns (of gate and up for GATED) and its eight waves
-// every eighth block of K; operands go from memory straight into registers,
-// each weight byte once, D blocks ahead, with no barrier in the loop; the
-// waves' sums are added in wave order.
-constexpr int kFewRows = 48, kFewWaves = 8;
+// Up to 64 rows of A: the weights' bytes are what counts.  A workgroup owns 16
+// columns (of gate and of up for GATED) and each of its waves a stretch of K.
+// A wave copies its blocks into a ring of its own in LDS, FD ahead, and waits
+// for its own copies alone: no barrier in the loop, no registers in flight,
+// and whole 128-byte lines (loads straight into registers, in the
+// instruction's layout of 16 rows by 64 bytes, reached 35 bytes a ns and CU;
+// this reaches 60).  The waves' sums are added in wave order.
+// NA: 8-row copies of A.
+constexpr int kFewRows = 64, kFewDepth = 2;
 
-template <int MT, bool FAST, bool GATED, int EPI>
-__global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GArgs a) {
-  constexpr int NB = GATED ? 2 : 1, D = MT == 1 && !GATED ? 3 : 2;
-  __shared__ float part[kFewWaves][NB][MT * 16][17];
+template <int NA, bool GATED> struct Few {
+  static constexpr int NB = GATED ? 2 : 1, MT = (NA + 1) / 2;
+  static constexpr int WAVES = NB + MT <= 4 ? 8 : NB + MT == 5 ? 6 : 5;   // as many as LDS holds
+  static constexpr int PER = 2 * NB + NA;                 // copies a block
+  static constexpr int SLOT = (NB + MT) * 2048;           // B rows, then A rows
+  static constexpr int SCB = MT * 512 + 256;              // scales of eight blocks: A rows, then B
+  static constexpr int RING = kFewDepth * SLOT + 2 * SCB; // bytes of a wave
+  static constexpr int PART = NB * MT * 16 * 17;          // a wave's sums (floats)
+  static constexpr int SMEM = WAVES * (RING > PART * 4 ? RING : PART * 4);
+};
+
+template <int NA, bool FAST, bool GATED, int EPI>
+__global__ __launch_bounds__((Few<NA, GATED>::WAVES * 64)) void few_rows_kernel(GArgs a) {
+  using F = Few<NA, GATED>;
+  constexpr int NB = F::NB, MT = F::MT;
+  __shared__ __attribute__((aligned(1024))) char S[F::SMEM];
   const int t = threadIdx.x, lane = t & 63, l15 = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int kp = 16 * (lane >> 4);
-  const uint8_t *ap[MT], *bp[NB];
-  const float *sap[MT], *sbp[NB];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {   // rows that do not exist: row 0, never stored
-    const int64_t m = i * 16 + l15 < a.M ? i * 16 + l15 : 0;
-    ap[i] = a.A + m * a.lda + kp;
-    sap[i] = a.sa + m * a.kb;
-  }
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    bp[b] = a.B[b] + min(n0 + l15, a.N - 1) * a.ldb[b] + kp;
-    sbp[b] = a.sb[b] + n0 / 128 * a.kb;
-  }
-  f32x4 acc[NB][MT];
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int nleft = (int)min((int64_t)16, a.N - n0), mleft = (int)a.M;
+  const int per = (a.kb + F::WAVES - 1) / F::WAVES;
+  const int kbeg = w * per, nblk = min(per, a.kb - kbeg);   // may be 0 or less
+  char* ring = S + w * F::RING;
+  const unsigned rbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)ring;
 
-  struct Raw { i32x4 x, y; };
-  Raw ra[D][MT], rb[D][NB];
-  float sa[D][MT], sb[D][NB];
-  const int full = (int)(a.K / 128);   // whole blocks
-  auto load = [&](int d, int kb) {
-    const int64_t k = (int64_t)kb * 128;
-    if (kb < full) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        __builtin_memcpy(&rb[d][b].x, bp[b] + k, 16);
-        __builtin_memcpy(&rb[d][b].y, bp[b] + k + 64, 16);
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        __builtin_memcpy(&ra[d][i].x, ap[i] + k, 16);
-        __builtin_memcpy(&ra[d][i].y, ap[i] + k + 64, 16);
-      }
-    } else {   // the rows end inside this block
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        rb[d][b].x = piece16(bp[b] - kp, k + kp, a.K, true);
-        rb[d][b].y = piece16(bp[b] - kp, k + kp + 64, a.K, true);
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        ra[d][i].x = piece16(ap[i] - kp, k + kp, a.K, true);
-        ra[d][i].y = piece16(ap[i] - kp, k + kp + 64, a.K, true);
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) sb[d][b] = sbp[b][kb];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) sa[d][i] = sap[i][kb];
+  // copy i of a block: eight rows of B (i < 2·NB) or A, lane l row l/8 of them,
+  // piece l%8 to slot l%8 as in the tile kernel; rows that do not exist copy
+  // the last one (their results are never stored)
+  auto base = [&](int i) -> const uint8_t* {
+    return i < 2 * NB ? a.B[i / 2] + n0 * a.ldb[i / 2] : a.A;
   };
+  auto offset = [&](int i) -> int64_t {
+    const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((i & 1) << 6);
+    return i < 2 * NB ? (int64_t)min((i & 1) * 8 + (lane >> 3), nleft - 1) * a.ldb[i / 2] + p16
+                      : (int64_t)min((i - 2 * NB) * 8 + (lane >> 3), mleft - 1) * a.lda + p16;
+  };
+  auto dest = [&](int slot, int i) { return slot * F::SLOT + i * 1024; };
+  uint32_t voff[F::PER];
 #pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (w + d * kFewWaves < a.kb) load(d, w + d * kFewWaves);
-  for (int k0 = w; k0 < a.kb; k0 += D * kFewWaves) {
+  for (int i = 0; i < F::PER; ++i) voff[i] = (uint32_t)offset(i);
+  const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;   // blocks from here on: bytewise
+  auto copy = [&](int j) {
+    const int slot = j % kFewDepth;
+    if (kbeg + j < last_wide) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const int kb = k0 + d * kFewWaves;
-      if (kb >= a.kb) break;
-      Frag<FAST> fb[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) fb[b].set(rb[d][b].x, rb[d][b].y);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        Frag<FAST> fa;
-        fa.set(ra[d][i].x, ra[d][i].y);
-        f32x4 p[NB];
-        contract(fb, fa, p);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const float s = sa[d][i] * sb[d][b];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[b][i][r] = __builtin_fmaf(p[b][r], s, acc[b][i][r]);
-        }
+      for (int i = 0; i < F::PER; ++i)
+        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :: "s"(rbase + (unsigned)dest(slot, i)), "v"(voff[i]),
+                        "s"(base(i) + (int64_t)(kbeg + j) * 128)
+                     : "memory");
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < F::PER; ++i) {
+        const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((i & 1) << 6);
+        const i32x4 v = piece16(base(i) + offset(i) - p16, (int64_t)(kbeg + j) * 128 + p16, a.K, true);
+        *reinterpret_cast<i32x4*>(ring + dest(slot, i) + lane * 16) = v;
       }
-      if (kb + D * kFewWaves < a.kb) load(d, kb + D * kFewWaves);
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    }
+  };
+  // scales of blocks 8·g..: eight rows by eight blocks a copy
+  auto copy_scales = [&](int g) {
+    const int r = lane >> 3, k = min(kbeg + 8 * g + (lane & 7), a.kb - 1);
+#pragma unroll
+    for (int i = 0; i < 2 * MT + 1; ++i) {
+      const float* p = i < 2 * MT ? a.sa + (int64_t)min(i * 8 + r, mleft - 1) * a.kb
+                                  : (r == 0 ? a.sb[0] : a.sb[NB - 1]) + n0 / 128 * a.kb;
+      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
+                   :: "s"(rbase + (unsigned)(kFewDepth * F::SLOT + (g & 1) * F::SCB + i * 256)), "v"(p + k)
+                   : "memory");
+    }
+  };
+
+  f32x4 acc[MT][NB];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (nblk > 0) {
+    copy_scales(0);
+#pragma unroll
+    for (int j = 0; j < kFewDepth; ++j)
+      if (j < nblk) copy(j);
+  }
+  const int row = l15 * 128 + (((lane >> 4) ^ ((l15 >> 1) & 7)) << 4);
+  for (int j = 0; j < nblk; ++j) {
+    // this block's copies have landed when no more are in flight than the
+    // later blocks' (scales among them only make the wait longer)
+    if (j + kFewDepth <= nblk) asm volatile("s_waitcnt vmcnt(%0)" :: "i"((kFewDepth - 1) * F::PER) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const char* q = ring + (j % kFewDepth) * F::SLOT + row;
+    const char* sc = ring + kFewDepth * F::SLOT + ((j >> 3) & 1) * F::SCB + (j & 7) * 4;
+    i32x4 x[NB + MT], y[NB + MT];
+#pragma unroll
+    for (int i = 0; i < NB + MT; ++i) {
+      x[i] = *reinterpret_cast<const i32x4*>(q + i * 2048);
+      y[i] = *reinterpret_cast<const i32x4*>(ring + (j % kFewDepth) * F::SLOT + (row ^ 64) + i * 2048);
+    }
+    float sa[MT], sb[NB];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sa[i] = *reinterpret_cast<const float*>(sc + (i * 16 + l15) * 32);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) sb[b] = *reinterpret_cast<const float*>(sc + MT * 512 + b * 32);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read: the slot may be written again
+    if ((j & 7) == 0 && j + 8 < nblk) copy_scales((j >> 3) + 1);
+    if (j + kFewDepth < nblk) copy(j + kFewDepth);
+    Frag<FAST> fb[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) fb[b].set(x[b], y[b]);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      Frag<FAST> fa;
+      fa.set(x[NB + i], y[NB + i]);
+      f32x4 p[NB];
+      contract(fb, fa, p);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float s = sa[i] * sb[b];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][b][r] = __builtin_fmaf(p[b][r], s, acc[i][b][r]);
+      }
     }
   }
+  __syncthreads();   // the sums go where the rings were
+  float* part = reinterpret_cast<float*>(S);
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) part[w][b][i * 16 + l15][4 * (lane >> 4) + r] = acc[b][i][r];
+      for (int r = 0; r < 4; ++r)
+        part[w * F::PART + ((b * MT + i) * 16 + l15) * 17 + 4 * (lane >> 4) + r] = acc[i][b][r];
   __syncthreads();
   const int c = t & 15;
+  if (c >= nleft) return;
   const int64_t n = n0 + c;
-  if (n >= a.N) return;
-  for (int m = t >> 4; m < MT * 16 && m < a.M; m += kFewWaves * 4) {
+  for (int m = t >> 4; m < MT * 16 && m < mleft; m += F::WAVES * 4) {
     float h[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       h[b] = 0.f;
 #pragma unroll
-      for (int q = 0; q < kFewWaves; ++q) h[b] += part[q][b][m][c];
+      for (int v = 0; v < F::WAVES; ++v) h[b] += part[v * F::PART + (b * MT * 16 + m) * 17 + c];
     }
-    float x = h[0];
-    if constexpr (GATED) x = activate(h[0], a.act) * h[NB - 1];
+    float o = h[0];
+    if constexpr (GATED) o = activate(h[0], a.act) * h[NB - 1];
     if constexpr (EPI == kPartial) {
-      a.P[(int64_t)m * a.N + n] = x;     // h itself: one partial, activated
+      a.P[(int64_t)m * a.N + n] = o;     // h itself: one partial, activated
     } else {
-      if (a.c_dt == GPTQ_F32) static_cast<float*>(a.C)[m * a.ldc + n] = x;
-      else if (a.c_dt == GPTQ_BF16) static_cast<__bf16*>(a.C)[m * a.ldc + n] = (__bf16)x;
-      else static_cast<_Float16*>(a.C)[m * a.ldc + n] = (_Float16)x;
+      if (a.c_dt == GPTQ_F32) static_cast<float*>(a.C)[m * a.ldc + n] = o;
+      else if (a.c_dt == GPTQ_BF16) static_cast<__bf16*>(a.C)[m * a.ldc + n] = (__bf16)o;
+      else static_cast<_Float16*>(a.C)[m * a.ldc + n] = (_Float16)o;
     }
   }
 }
@@ -672,7 +713,11 @@ constexpr TileCost kTiles[] = {
 };
 constexpr int kTileKinds = 4;
 constexpr double kLaunch = 4.0, kJoin = 3.5, kJoinBytes = 4.5e6;   // us, us, bytes per us
-constexpr double kFewLaunch = 2.5, kFewCopies = 7.0e3;             // us, KB of operands per us
+// Few rows, the same way: a workgroup's start and end, its copies at the rate
+// one CU takes them (KB a us), or its waves' instructions (two waves a SIMD;
+// cycles a block and wave: conversions, products, the rest), or all weights
+// from memory (KB a us).
+constexpr double kFewLaunch = 2.3, kFewGroup = 1.0, kFewCopies = 75.0, kFewWeights = 7e3, kClock = 2100.0;
 
 struct Plan { int tile; int splits, kper; };   // tile -1: few rows
 
@@ -685,10 +730,15 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool exact, bool codes
   Plan best{kTileKinds - 1, 1, (int)kb};
   double least = 1e300;
   if (M <= kFewRows && (!codes || ws)) {
-    const double mt = (double)ceil_div(M, 16);
-    // a piece with few real rows hits the first-level cache
-    const double kbytes = (double)ceil_div(N, 16) * kb * 2 * (nb + mt * std::min<double>(1.0, M / 12.0));
-    least = kFewLaunch + kbytes / kFewCopies + (codes ? kJoin : 0);
+    const int mt = (int)ceil_div(M, 16), waves = nb + mt <= 4 ? 8 : nb + mt == 5 ? 6 : 5;
+    const int64_t groups = ceil_div(N, 16);
+    const int fit = nb + mt == 2 ? 2 : 1, here = (int)std::min<int64_t>(fit, ceil_div(groups, 256));
+    const double copied = 2.0 * kb * (nb + (M <= 8 ? 0.5 : mt)) / kFewCopies;
+    const double cycles = exact ? 1.25 * (64 * (nb + mt) + 80 * nb * mt + 150) : 48 * nb * mt + 200;
+    const double issued = 2.0 * (double)ceil_div(kb, waves) * cycles / kClock;
+    least = kFewLaunch + (codes ? kJoin : 0) +
+            std::max((double)ceil_div(groups, 256 * here) * (kFewGroup + here * std::max(copied, issued)),
+                     2.0 * groups * kb * nb / kFewWeights);
     best = {-1, 1, (int)kb};
   }
   for (int i = 0; i < kTileKinds; ++i) {
@@ -741,10 +791,14 @@ hipError_t launch_kind(GArgs& a, const Plan& p, hipStream_t s) {
 }
 
 template <bool FAST, bool GATED, int EPI> hipError_t launch_few(const GArgs& a, hipStream_t s) {
-  const unsigned grid = (unsigned)ceil_div(a.N, 16), nt = kFewWaves * 64;
-  if (a.M <= 16) few_rows_kernel<1, FAST, GATED, EPI><<<grid, nt, 0, s>>>(a);
-  else if (a.M <= 32) few_rows_kernel<2, FAST, GATED, EPI><<<grid, nt, 0, s>>>(a);
-  else few_rows_kernel<3, FAST, GATED, EPI><<<grid, nt, 0, s>>>(a);
+  const unsigned grid = (unsigned)ceil_div(a.N, 16);
+#define GQ_FEW(NA) few_rows_kernel<NA, FAST, GATED, EPI><<<grid, Few<NA, GATED>::WAVES * 64, 0, s>>>(a)
+  if (a.M <= 8) GQ_FEW(1);
+  else if (a.M <= 16) GQ_FEW(2);
+  else if (a.M <= 32) GQ_FEW(4);
+  else if (a.M <= 48) GQ_FEW(6);
+  else GQ_FEW(8);
+#undef GQ_FEW
   return hipGetLastError();
 }
 

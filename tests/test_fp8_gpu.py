@@ -222,7 +222,8 @@ SHAPES = [(*s, ["f32", "bf16", "f16"][i % 3]) for i, s in enumerate(SHAPES)] + [
     (54, 122, 204, "bf16"), (51, 126, 2303, "f16"), (50, 122, 1384, "f32"), (229, 129, 5362, "bf16"),
     (480, 129, 1958, "f32"), (385, 7173, 211, "bf16"), (301, 6540, 200, "f32"), (66, 2803, 6309, "f16"),
     (65, 1350, 5633, "f32"), (1951, 6168, 203, "f16"), (131, 5510, 7906, "f32"), (3216, 1423, 7218, "bf16"),
-    (20, 17000, 300, "bf16"), (47, 2000, 640, "bf16"), (16, 130, 65536, "bf16"), (49, 130, 65530, "f32")]
+    (20, 17000, 300, "bf16"), (47, 2000, 640, "bf16"), (16, 130, 65536, "bf16"), (49, 130, 65530, "f32"),
+    (65, 128, 1291, "f32"), (20, 300, 700, "f32"), (8, 1000, 2000, "f16"), (9, 1000, 2000, "f32")]
 
 
 @pytest.mark.parametrize("M,N,K,dtype", SHAPES)
@@ -257,7 +258,9 @@ GATED = [(*s, ["f32", "bf16", "f16"][i % 3]) for i, s in enumerate(GATED)] + [
     (67, 231, 5226, "silu", "bf16"), (66, 464, 1924, "gelu_tanh", "f32"), (213, 6510, 200, "silu", "bf16"),
     (165, 5605, 207, "silu", "f32"), (65, 3284, 5935, "silu", "f16"), (67, 1421, 3204, "silu", "f32"),
     (1282, 4452, 203, "silu", "bf16"), (135, 2942, 7038, "gelu", "f32"), (456, 4178, 6348, "silu", "bf16"),
-    (20, 9000, 300, "gelu", "bf16")]
+    (20, 9000, 300, "gelu", "bf16"), (65, 120, 2194, "silu", "bf16"), (65, 121, 1484, "silu", "f32"),
+    (396, 4716, 4274, "silu", "f32"), (166, 5484, 258, "gelu_tanh", "f32"), (20, 300, 700, "silu", "f32"),
+    (40, 300, 700, "silu", "f32"), (8, 1000, 2000, "silu", "f32"), (64, 1000, 2000, "silu", "f32")]
 
 
 @pytest.mark.parametrize("M,N,K,act,dtype", GATED)
