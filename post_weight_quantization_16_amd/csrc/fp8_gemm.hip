@@ -82,20 +82,31 @@ __device__ __forceinline__ void contract(const Frag<false>* b, const Frag<false>
       q[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[g].v[i], a.v[i], q[g], 0, 0, 0);
 }
 
-// 16 bytes of a row from byte k on; bytes past the row's K and rows that do
-// not exist are zero.
-__device__ __forceinline__ i32x4 piece16(const uint8_t* row, int64_t k, int64_t K, bool ok) {
+// 16 bytes of a row from byte k on, zeros past the row's K bytes.  A piece that
+// K cuts is loaded so that it ends at K, and shifted.
+__device__ __forceinline__ i32x4 piece16(const uint8_t* row, int64_t k, int64_t K) {
   i32x4 v = {0, 0, 0, 0};
-  if (ok && k + 16 <= K) {
-    __builtin_memcpy(&v, row + k, 16);
-  } else if (ok && k < K) {
-    uint64_t lo = 0, hi = 0;
-#pragma unroll 1
-    for (int i = 0; i < (int)(K - k); ++i) {
-      const uint64_t x = (uint64_t)row[k + i] << (8 * (i & 7));
-      if (i < 8) lo |= x; else hi |= x;
+  if (k >= K) return v;
+  if (K >= 16) {
+    const int cut = (int)max((int64_t)0, k + 16 - K);   // bytes past K
+    uint64_t q[2];
+    __builtin_memcpy(q, row + k - cut, 16);
+    const int sh = 8 * (cut & 7);
+    if (cut >= 8) {
+      q[0] = q[1];
+      q[1] = 0;
     }
-    v = i32x4{(int)(uint32_t)lo, (int)(uint32_t)(lo >> 32), (int)(uint32_t)hi, (int)(uint32_t)(hi >> 32)};
+    if (sh) q[0] = (q[0] >> sh) | (q[1] << (64 - sh));
+    q[1] >>= sh;
+    v = i32x4{(int)(uint32_t)q[0], (int)(uint32_t)(q[0] >> 32), (int)(uint32_t)q[1], (int)(uint32_t)(q[1] >> 32)};
+  } else {
+    uint64_t q[2] = {0, 0};   // k == 0
+#pragma unroll 1
+    for (int i = 0; i < (int)K; ++i) {
+      const uint64_t x = (uint64_t)row[i] << (8 * (i & 7));
+      if (i < 8) q[0] |= x; else q[1] |= x;
+    }
+    v = i32x4{(int)(uint32_t)q[0], (int)(uint32_t)(q[0] >> 32), (int)(uint32_t)q[1], (int)(uint32_t)(q[1] >> 32)};
   }
   return v;
 }
@@ -151,6 +162,9 @@ template <int BM, int BN, int WM, int WN, int NS> struct Tile {
   static constexpr int SCOPIES = BM / 8 + 1;            // copies of eight blocks' scales
   static_assert(SEGS % WAVES == 0 && NS >= 2 && NS <= 4, "copy plan");
   static_assert((NS - 2) * PER <= 63, "vmcnt range");
+  // waves a SIMD gets from the workgroups that fit in a CU's LDS: the
+  // registers must leave room for them
+  static constexpr int WPE = 163840 / SMEM * WAVES / 4;
 };
 
 // Waits until all copies but the last `ahead` stages' (loads complete in issue
@@ -177,7 +191,7 @@ __device__ __forceinline__ void tile_of(uint32_t L, uint32_t total, uint32_t tm,
 enum { kStore = 0, kPartial = 1, kCodes = 2 };
 
 template <int BM, int BN, int WM, int WN, int NS, bool FAST, bool GATED, int EPI, int DT>
-__global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel(GArgs a) {
+__global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, WN, NS>::WPE)) void tile_kernel(GArgs a) {
   using T = Tile<BM, BN, WM, WN, NS>;
   constexpr int MI = T::MI, NI = T::NI, NB = GATED ? 2 : 1;
   // B pieces a step takes: the exact form's four instructions depend on each
@@ -225,7 +239,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
     for (int i = 0; i < T::PER; ++i) voff[i] = (uint32_t)seg_offset(w * T::PER + i, lane);
   }
   const unsigned sbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)S;
-  const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;   // blocks from here on: bytewise
+  const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;   // blocks from here on: through registers
   // the wave's copies of the scales of blocks 8·g.. of this split
   auto copy_scales = [&](int g) {
     int l = lane;
@@ -241,7 +255,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
                    :: "s"(sbase + T::SCALES + (unsigned)((g & 1) * T::SCB + idx * 256)), "v"(p + k) : "memory");
     }
   };
-  // copies i0 .. i1 - 1 of a stage (bytewise: all of them with the first)
+  // copies i0 .. i1 - 1 of a stage (through registers: all of them with the first)
   auto copy = [&](int st, int i0, int i1) {
     const unsigned buf = (unsigned)((st % NS) * T::SB);
     if (kbeg + st < last_wide) {
@@ -258,14 +272,21 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), 2) void tile_kernel
                      : "memory");
       }
     } else if (i0 == 0) {
-      // rows that end inside this block, or start at odd addresses
+      // rows that end inside this block, or start at odd addresses: through
+      // registers, few at a time (more would cost workgroups a CU)
+      constexpr int U = FAST && T::PER % 2 == 0 ? 2 : 1;
 #pragma unroll 1
-      for (int i = 0; i < T::PER; ++i) {
-        const int seg = w * T::PER + i;
-        const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((seg & 1) << 6);
-        const int64_t k = (int64_t)(kbeg + st) * 128 + p16;
-        const i32x4 v = piece16(seg_base(seg) + seg_offset(seg, lane) - p16, k, a.K, true);
-        *reinterpret_cast<i32x4*>(S + buf + seg * 1024 + lane * 16) = v;
+      for (int g = 0; g < T::PER; g += U) {
+        i32x4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int seg = w * T::PER + g + u;
+          const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((seg & 1) << 6);
+          v[u] = piece16(seg_base(seg) + seg_offset(seg, lane) - p16, (int64_t)(kbeg + st) * 128 + p16, a.K);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          *reinterpret_cast<i32x4*>(S + buf + (w * T::PER + g + u) * 1024 + lane * 16) = v[u];
       }
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
@@ -532,7 +553,7 @@ __global__ __launch_bounds__((Few<NA, GATED>::WAVES * 64)) void few_rows_kernel(
   uint32_t voff[F::PER];
 #pragma unroll
   for (int i = 0; i < F::PER; ++i) voff[i] = (uint32_t)offset(i);
-  const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;   // blocks from here on: bytewise
+  const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;   // blocks from here on: through registers
   auto copy = [&](int j) {
     const int slot = j % kFewDepth;
     if (kbeg + j < last_wide) {
@@ -543,12 +564,14 @@ __global__ __launch_bounds__((Few<NA, GATED>::WAVES * 64)) void few_rows_kernel(
                         "s"(base(i) + (int64_t)(kbeg + j) * 128)
                      : "memory");
     } else {
-#pragma unroll 1
+      i32x4 v[F::PER];
+#pragma unroll
       for (int i = 0; i < F::PER; ++i) {
         const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((i & 1) << 6);
-        const i32x4 v = piece16(base(i) + offset(i) - p16, (int64_t)(kbeg + j) * 128 + p16, a.K, true);
-        *reinterpret_cast<i32x4*>(ring + dest(slot, i) + lane * 16) = v;
+        v[i] = piece16(base(i) + offset(i) - p16, (int64_t)(kbeg + j) * 128 + p16, a.K);
       }
+#pragma unroll
+      for (int i = 0; i < F::PER; ++i) *reinterpret_cast<i32x4*>(ring + dest(slot, i) + lane * 16) = v[i];
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
   };
