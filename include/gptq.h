@@ -405,7 +405,8 @@ int gptq_w4a16_gemm(const void* A, int a_dtype, int64_t M, int64_t K, int64_t ld
  *  to even); a block that holds a NaN or an infinity gets a NaN scale and NaN
  *  codes, so that what is computed from it is NaN.
  * rows (or M) == 0 is a no-op in every call: the tensors of that side may be
- * NULL.  All calls are asynchronous, return argument errors and GPTQ_ERR_HIP
+ * NULL.  Outputs must not overlap inputs or each other unless a call says so.
+ * All calls are asynchronous, return argument errors and GPTQ_ERR_HIP
  * only, and give the same bits on every run. */
 
 /* Quantize X into a block-scaled matrix.
@@ -422,7 +423,7 @@ int gptq_fp8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, in
  *  X, R       [rows x cols] of x_dtype, row strides ld_x, ld_r >= cols; R may
  *             be NULL.
  *  gamma      [cols] of g_dtype: x_dtype or GPTQ_F32.
- *  eps        finite, >= 0.
+ *  eps        finite, >= 0 (with 0, a row of zeros gives NaN: 0/0).
  *  H          out [rows x cols] of x_dtype, row stride ld_h: the sum that the
  *             next residual addition takes; may be NULL; may be X or R itself
  *             (same address and stride), else must not overlap them.

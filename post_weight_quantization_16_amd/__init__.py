@@ -10,6 +10,9 @@ memory and streams only).
     hessian_accumulate(H, X)                      # H += 2 XᵀX, X token-major
     prep = prepare_hinv(H, params)                # U, perm, dead
     out = quantize_layer(W, prep, params)         # qweight, scales, zeros, ...
+
+8-bit floating point (block-scaled e4m3 matrices, Fp8Matrix): fp8_quantize,
+rmsnorm_fp8, fp8_gemm, fp8_gated_gemm.
 """
 from __future__ import annotations
 

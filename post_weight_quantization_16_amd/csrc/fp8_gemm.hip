@@ -139,6 +139,14 @@ __device__ __forceinline__ uint32_t mag_bits(float x) {
 }
 
 // ---------------------------------------------------------------- tile kernel
+// Bound: at 4096 x 28672 x 8192 to bf16 (fp8 instructions, 256 x 256 tiles) 850
+// us, 2.26 PFLOP/s; the matrix cores are busy 55 % of the cycles, at the 1.7
+// GHz that the power budget leaves.  The stages' copies out of L2 (64 KB a stage and
+// CU, 9 TB/s in all) and the LDS reads beside them set the pace: without the
+// copies it runs at 2.87, without the reads at 2.84 PFLOP/s.  The exact form
+// (2048 x 28672 x 8192 gated to codes: 1.48 ms, 1.30 PFLOP/s) is at 0.93 of
+// the rate that a large bf16 product reaches here; half its time is issue of
+// the conversions and adds beside the products.
 // BM x BN tile of C per workgroup, waves of WM x WN, K in stages of one block
 // in a ring of NS stage buffers.  Stages go from memory straight into LDS
 // (global_load_lds: no registers, no LDS store instructions), NS-1 ahead.
@@ -509,7 +517,11 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
 // for its own copies alone: no barrier in the loop, no registers in flight,
 // and whole 128-byte lines (loads straight into registers, in the
 // instruction's layout of 16 rows by 64 bytes, reached 35 bytes a ns and CU;
-// this reaches 60).  The waves' sums are added in wave order.
+// this reaches 75).  The waves' sums are added in wave order.
+// Bound: the weights' bytes, and at more than 16 rows the copies of A beside
+// them.  28672 x 8192 at 16 rows: 34 us, 6.8 TB/s out of the memory-side
+// cache; 11008 x 4096 gate and up at 4 rows, from memory: 19 us, 4.7 TB/s;
+// 37 x 4000 x 11008 to fp32: 12.4 us.
 // NA: 8-row copies of A.
 constexpr int kFewRows = 64, kFewDepth = 2;
 
@@ -674,7 +686,8 @@ __global__ __launch_bounds__((Few<NA, GATED>::WAVES * 64)) void few_rows_kernel(
 // ---------------------------------------------------------------- joining partial sums
 // One thread per eight columns: the partials in split order, then the
 // activation (gated, not yet activated) and C, or a block's codes and scale
-// (16 lanes a block).
+// (16 lanes a block).  A launch of its own, 2 to 4 us where the partials are
+// small; the cost model charges it to every split.
 template <bool GATED, bool CODES>
 __global__ __launch_bounds__(256) void join_kernel(GArgs a, int splits) {
   constexpr int NB = GATED ? 2 : 1;

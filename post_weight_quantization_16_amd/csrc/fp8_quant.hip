@@ -29,6 +29,8 @@ __device__ __forceinline__ void encode8(const float (&v)[8], float s, uint32_t& 
 
 // Activations: 16 lanes per 1 x 128 block, eight columns a lane.  A workgroup
 // of 256 threads takes 2^lg blocks of a row side by side and 16 >> lg rows.
+// Bound by memory: 517 x 11008 fp16 in 7.0 us (2.4 TB/s, mostly the launch's
+// ramp), 1 x 4096 in 2.0 us (a launch).
 template <int DT>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QArgs a, int lg, uint32_t chunks) {
   typedef typename Elem<DT>::type T;
@@ -51,7 +53,10 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QArgs a, int lg, uin
 }
 
 // Weights: one workgroup per 128 x 128 block, 16 lanes across and 16 rows at
-// a time, the whole block in registers (64 values a thread).
+// a time, the whole block in registers (64 values a thread), so the input is
+// read once.  Bound by memory: 28672 x 8192 bf16 in 144 us, 4.9 TB/s, the rate
+// of a large copy; the fp64 quotients (about twelve instructions a value) hide
+// behind it.
 template <int DT>
 __global__ __launch_bounds__(256) void quantize_block_kernel(QArgs a) {
   typedef typename Elem<DT>::type T;
@@ -105,7 +110,8 @@ struct NArgs {
 // The sum of squares, 1/sqrt and y are fp64: the sum because rows are long,
 // y because codes next to a border of e4m3 would change with fp32's rounding
 // (the fp64 rate of gfx950 is that of unpacked fp32, and the kernel is bound
-// by memory).
+// by memory: 16384 x 4096 bf16 with a residual in 100 us, 4.7 TB/s, against
+// 4.9 of a large copy; one row in 3.7 us).
 template <int DT, int GDT, int NT, int P>
 __global__ __launch_bounds__(NT) void rmsnorm_kernel(NArgs a) {
   typedef typename Elem<DT>::type T;
