@@ -97,8 +97,14 @@ __device__ __forceinline__ void load8(const typename Elem<DT>::type* p, int n, f
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = Elem<DT>::up(x[i]);
   } else {
+    // one element a load, all in flight together (a branch for each would
+    // wait eight times)
+    if (n > 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem<DT>::up(p[i]) : 0.f;
+      for (int i = 0; i < 8; ++i) x[i] = p[i < n ? i : n - 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem<DT>::up(x[i]) : 0.f;
   }
 }
 template <int DT>
