@@ -20,17 +20,26 @@ typedef __attribute__((ext_vector_type(8))) int i32x8;
 constexpr int kFp8Block = 128;        // columns of a block (and rows, for weights)
 constexpr float kE4m3Max = 448.f;
 
-// Scale of a block from its largest magnitude (NaN or infinite: NaN).
+// Scale of a block from its largest magnitude (NaN or infinite: NaN).  For an
+// fp32 amax the product with 1/448 rounds to fp32 as the quotient does: amax/7
+// is either exact in fp32 or at least 2^-28 of itself away from a border.
 __device__ __forceinline__ float e4m3_scale(double amax) {
-  const float s = fmaxf((float)(amax / 448.0), 1.17549435e-38f);
+  const float s = fmaxf((float)(amax * (1.0 / 448.0)), 1.17549435e-38f);
   return __builtin_isfinite(amax) ? s : __builtin_nanf("");
 }
 
+// 1/s for e4m3_quotient, to 2^-40 or better (the estimate's 2^-20 or better,
+// squared): what is left enters the quotient squared again.
+__device__ __forceinline__ double e4m3_inverse(float s) {
+  const double sd = (double)s, r = __builtin_amdgcn_rcp(sd);
+  return __builtin_fma(__builtin_fma(-sd, r, 1.0), r, r);
+}
+
 // x/s as a float that rounds to e4m3 as the exact quotient does: the quotient
-// in fp64 (inv = 1/s; one Newton step makes it the correctly rounded one, so
-// exact ties stay ties), its last 32 bits folded into a sticky bit above
-// them, which leaves a value fp32 holds exactly and keeps the side of every
-// border.  fp32 alone would move about one code in 10^6 over a border.
+// in fp64 (one correction by the exact remainder, so ties stay ties), its last
+// 32 bits folded into a sticky bit above them, which leaves a value fp32 holds
+// exactly and keeps the side of every border.  fp32 alone would move about one
+// code in 10^6 over a border.
 __device__ __forceinline__ float e4m3_quotient(double x, double s, double inv) {
   double q = x * inv;
   q = __builtin_fma(__builtin_fma(-q, s, x), inv, q);
@@ -85,34 +94,41 @@ template <> struct Elem<GPTQ_F16> {
   static __device__ __forceinline__ _Float16 down(float x) { return (_Float16)x; }
 };
 
-// Eight consecutive elements, `n` of them present (the others are zero).
+// Eight consecutive elements as stored, `n` of them present (the others are
+// zero).
 // Full pieces are copied whole at whatever alignment the caller's rows have:
 // gfx950 loads and stores wide words at any byte address in global memory.
 template <int DT>
-__device__ __forceinline__ void load8(const typename Elem<DT>::type* p, int n, float (&v)[8]) {
+__device__ __forceinline__ void load8_raw(const typename Elem<DT>::type* p, int n,
+                                          typename Elem<DT>::type (&x)[8]) {
   typedef typename Elem<DT>::type T;
-  T x[8];
   if (n >= 8) {
     __builtin_memcpy(x, p, sizeof x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = Elem<DT>::up(x[i]);
   } else {
     // one element a load, all in flight together (a branch for each would
     // wait eight times)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (T)0.f;
     if (n > 0) {
+      T y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = p[i < n ? i : n - 1];
+      for (int i = 0; i < 8; ++i) y[i] = p[i < n ? i : n - 1];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = i < n ? y[i] : (T)0.f;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem<DT>::up(x[i]) : 0.f;
   }
 }
+// The same, widened.
 template <int DT>
-__device__ __forceinline__ void store8(typename Elem<DT>::type* p, int n, const float (&v)[8]) {
-  typedef typename Elem<DT>::type T;
-  T x[8];
+__device__ __forceinline__ void load8(const typename Elem<DT>::type* p, int n, float (&v)[8]) {
+  typename Elem<DT>::type x[8];
+  load8_raw<DT>(p, n, x);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = Elem<DT>::down(v[i]);
+  for (int i = 0; i < 8; ++i) v[i] = Elem<DT>::up(x[i]);
+}
+template <int DT>
+__device__ __forceinline__ void store8_raw(typename Elem<DT>::type* p, int n,
+                                           const typename Elem<DT>::type (&x)[8]) {
   if (n >= 8) {
     __builtin_memcpy(p, x, sizeof x);
   } else {
@@ -120,6 +136,13 @@ __device__ __forceinline__ void store8(typename Elem<DT>::type* p, int n, const 
     for (int i = 0; i < 8; ++i)
       if (i < n) p[i] = x[i];
   }
+}
+template <int DT>
+__device__ __forceinline__ void store8(typename Elem<DT>::type* p, int n, const float (&v)[8]) {
+  typename Elem<DT>::type x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = Elem<DT>::down(v[i]);
+  store8_raw<DT>(p, n, x);
 }
 __device__ __forceinline__ void store_codes8(uint8_t* p, int n, uint32_t lo, uint32_t hi) {
   if (n >= 8) {

@@ -487,7 +487,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
 #pragma unroll
       for (int q = 0; q < BN / WN; ++q) u = max(u, top[q * BM + ml]);
       const float s = e4m3_scale((double)__builtin_bit_cast(float, u));
-      const double sd = (double)s, inv = 1.0 / sd;
+      const double sd = (double)s, inv = e4m3_inverse(s);
       if (ml >= mleft) continue;
       if (wn == 0 && lane < 16) a.sc[(m0 + ml) * a.nb + bn] = s;
 #pragma unroll
@@ -718,7 +718,7 @@ __global__ __launch_bounds__(256) void join_kernel(GArgs a, int splits) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) u = max(u, mag_bits(h[0][i]));
     const float s = e4m3_scale((double)__builtin_bit_cast(float, row16_max_u32(u)));
-    const double sd = (double)s, inv = 1.0 / sd;
+    const double sd = (double)s, inv = e4m3_inverse(s);
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = e4m3_quotient((double)h[0][i], sd, inv);

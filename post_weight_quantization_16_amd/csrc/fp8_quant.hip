@@ -19,7 +19,7 @@ __device__ __forceinline__ uint32_t mag_bits(float x) {
 }
 
 __device__ __forceinline__ void encode8(const float (&v)[8], float s, uint32_t& lo, uint32_t& hi) {
-  const double sd = (double)s, inv = 1.0 / sd;
+  const double sd = (double)s, inv = e4m3_inverse(s);
   float q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) q[i] = e4m3_quotient((double)v[i], sd, inv);
@@ -98,7 +98,7 @@ struct NArgs {
   const void* X; int64_t ld_x;
   const void* R; int64_t ld_r;   // residual or null
   const void* gamma;
-  int64_t rows, cols; float eps;
+  int64_t rows, cols; double inv_cols, eps;
   void* S; int64_t ld_s;         // h, or null
   void* Y; int64_t ld_y;         // y in h's type, or null
   uint8_t* codes; int64_t ld_c;  // or null, with scales
@@ -119,28 +119,37 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NArgs a) {
   __shared__ double part[NT / 64];
   const int t = threadIdx.x;
   const int64_t row = blockIdx.x;
-  float v[P][8];
-  auto width = [&](int i) {
-    return (int)max((int64_t)0, min((int64_t)8, a.cols - (int64_t)(t + i * NT) * 8));
-  };
+  auto col = [&](int i) { return (t + i * NT) * 8; };
+  auto width = [&](int i) { return max(0, min(8, (int)a.cols - col(i))); };
+  T v[P][8];
 #pragma unroll
   for (int i = 0; i < P; ++i)
-    load8<DT>(static_cast<const T*>(a.X) + row * a.ld_x + (int64_t)(t + i * NT) * 8, width(i), v[i]);
+    load8_raw<DT>(static_cast<const T*>(a.X) + row * a.ld_x + col(i), width(i), v[i]);
+  // γ arrives with the row where registers allow, else from the cache later
+  constexpr bool EARLY = P <= 2;
+  G gm[EARLY ? P : 1][8];
+  if constexpr (EARLY) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) load8_raw<GDT>(static_cast<const G*>(a.gamma) + col(i), width(i), gm[i]);
+  }
   if (a.R) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      float r[8];
-      load8<DT>(static_cast<const T*>(a.R) + row * a.ld_r + (int64_t)(t + i * NT) * 8, width(i), r);
+      T r[8];
+      load8_raw<DT>(static_cast<const T*>(a.R) + row * a.ld_r + col(i), width(i), r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = Elem<DT>::up(Elem<DT>::down(v[i][j] + r[j]));
+      for (int j = 0; j < 8; ++j) v[i][j] = Elem<DT>::down(Elem<DT>::up(v[i][j]) + Elem<DT>::up(r[j]));
     }
   }
   double ss = 0.0;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    if (a.S) store8<DT>(static_cast<T*>(a.S) + row * a.ld_s + (int64_t)(t + i * NT) * 8, width(i), v[i]);
+    if (a.S) store8_raw<DT>(static_cast<T*>(a.S) + row * a.ld_s + col(i), width(i), v[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)v[i][j], (double)v[i][j], ss);
+    for (int j = 0; j < 8; ++j) {
+      const double x = (double)Elem<DT>::up(v[i][j]);
+      ss = __builtin_fma(x, x, ss);
+    }
   }
   ss += dpp_d<kRor8>(ss); ss += dpp_d<kRor4>(ss); ss += dpp_d<kRor2>(ss); ss += dpp_d<kRor1>(ss);
   ss += __shfl_xor(ss, 16);
@@ -152,29 +161,42 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NArgs a) {
 #pragma unroll
     for (int w = 0; w < NT / 64; ++w) ss += part[w];
   }
-  const double rstd = 1.0 / __builtin_sqrt(ss / (double)a.cols + (double)a.eps);
+  // 1/sqrt: the estimate and two Newton steps (they would turn the estimates
+  // of 0 and infinity, infinity and 0, into NaN)
+  const double x = __builtin_fma(ss, a.inv_cols, a.eps);
+  double rstd = __builtin_amdgcn_rsq(x);
+  if (x > 0.0 && x < __builtin_inf()) {
+    rstd *= __builtin_fma(-0.5 * x * rstd, rstd, 1.5);
+    rstd *= __builtin_fma(-0.5 * x * rstd, rstd, 1.5);
+  }
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int n = width(i);
-    const int64_t col = (int64_t)(t + i * NT) * 8;
-    float g[8];
-    load8<GDT>(static_cast<const G*>(a.gamma) + col, n, g);
+    if constexpr (P >= 4) {   // widened anew: kept from the first pass, the row takes four times its size
+      uint32_t u[sizeof v[i] / 4];
+      __builtin_memcpy(u, v[i], sizeof u);
+#pragma unroll
+      for (int k = 0; k < (int)(sizeof u / 4); ++k) asm volatile("" : "+v"(u[k]));
+      __builtin_memcpy(v[i], u, sizeof u);
+    }
+    G g[8];
+    if constexpr (!EARLY) load8_raw<GDT>(static_cast<const G*>(a.gamma) + col(i), n, g);
     double y[8], m = 0.0, bad = 0.0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      y[j] = (double)v[i][j] * rstd * (double)g[j];
+      y[j] = (double)Elem<DT>::up(v[i][j]) * rstd * (double)Elem<GDT>::up(EARLY ? gm[EARLY ? i : 0][j] : g[j]);
       m = __builtin_fmax(m, __builtin_fabs(y[j]));
       bad = __builtin_fma(y[j], 0.0, bad);   // NaN if y is NaN or infinite
     }
     // columns past the row are zeros, but with rstd = NaN or inf they are NaN:
     // then so is the row
     if (a.Y) {
-      float f[8];
+      T f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = (float)y[j];
-      store8<DT>(static_cast<T*>(a.Y) + row * a.ld_y + col, n, f);
+      for (int j = 0; j < 8; ++j) f[j] = Elem<DT>::down((float)y[j]);
+      store8_raw<DT>(static_cast<T*>(a.Y) + row * a.ld_y + col(i), n, f);
     }
-    if (!a.codes) continue;
+    if (!a.codes) continue;   // the whole grid alike
     m = __builtin_fmax(m, dpp_d<kRor8>(m));
     m = __builtin_fmax(m, dpp_d<kRor4>(m));
     m = __builtin_fmax(m, dpp_d<kRor2>(m));
@@ -182,12 +204,12 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NArgs a) {
     bad += dpp_d<kRor8>(bad); bad += dpp_d<kRor4>(bad);
     bad += dpp_d<kRor2>(bad); bad += dpp_d<kRor1>(bad);
     const float s = e4m3_scale(m + bad);
-    const double sd = (double)s, inv = 1.0 / sd;
+    const double sd = (double)s, inv = e4m3_inverse(s);
     float q[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) q[j] = e4m3_quotient(y[j], sd, inv);
     if (n > 0)
-      store_codes8(a.codes + row * a.ld_c + col, n, e4m3_pack4(q[0], q[1], q[2], q[3]),
+      store_codes8(a.codes + row * a.ld_c + col(i), n, e4m3_pack4(q[0], q[1], q[2], q[3]),
                    e4m3_pack4(q[4], q[5], q[6], q[7]));
     if ((t & 15) == 0 && n > 0) a.scales[row * a.kb + (t + i * NT) / 16] = s;
   }
@@ -215,6 +237,7 @@ template <int DT, int GDT> hipError_t launch_rmsnorm(const NArgs& a, hipStream_t
   const unsigned grid = (unsigned)a.rows;
 #define GQ_NORM(NT, P) rmsnorm_kernel<DT, GDT, NT, P><<<grid, NT, 0, s>>>(a)
   if (pieces <= 64) GQ_NORM(64, 1);
+  else if (pieces <= 128) GQ_NORM(128, 1);
   else if (pieces <= 256) GQ_NORM(256, 1);
   else if (pieces <= 512) GQ_NORM(256, 2);
   else if (pieces <= 1024) GQ_NORM(512, 2);
@@ -242,7 +265,7 @@ hipError_t rmsnorm_fp8_launch(const void* X, int64_t ld_x, const void* R, int64_
                               const void* gamma, int g_dt, int64_t rows, int64_t cols, float eps,
                               void* S, int64_t ld_s, void* Y, int64_t ld_y, uint8_t* codes,
                               int64_t ld_c, float* scales, hipStream_t s) {
-  const NArgs a{X, ld_x, R, ld_r, gamma, rows, cols, eps, S, ld_s, Y, ld_y, codes, ld_c, scales,
+  const NArgs a{X, ld_x, R, ld_r, gamma, rows, cols, 1.0 / (double)cols, (double)eps, S, ld_s, Y, ld_y, codes, ld_c, scales,
                 ceil_div(cols, kFp8Block)};
   if (dt == GPTQ_F32) return launch_rmsnorm<GPTQ_F32, GPTQ_F32>(a, s);
   if (dt == GPTQ_BF16)
