@@ -544,7 +544,9 @@ def _t8():
     global _T
     if _T is None:
         torch = _torch()
-        _T = (torch.empty, torch.float8_e4m3fn, torch.float32, torch.cuda.current_device,
+        if torch.cuda.is_available():
+            torch.cuda.init()   # the two look-ups below take it for granted
+        _T = (torch.empty, torch.float8_e4m3fn, torch.float32, torch._C._cuda_getDevice,
               torch._C._cuda_getCurrentRawStream,
               {torch.float32: _native.F32, torch.bfloat16: _native.BF16, torch.float16: _native.F16})
     return _T
@@ -567,7 +569,7 @@ def _fp8_arg(m: Fp8Matrix, name, block_rows, device=None):
     if m.block_rows != block_rows:
         raise ValueError(f"{name} must have block_rows {block_rows} (got {m.block_rows})")
     c, s = m.codes, m.scales
-    _, e4m3, f32 = _t8()[:3]
+    _, e4m3, f32, _, _, _ = _t8()
     if c.dtype != e4m3:
         raise ValueError(f"{name}.codes must be float8_e4m3fn (got {c.dtype})")
     ld = _fp8_rows(c, name)
@@ -665,8 +667,10 @@ def rmsnorm_fp8(X, gamma, eps: float = 1e-6, residual=None, want_q: bool = True,
     h, ld_r, ld_h, hp = X, 0, 0, None
     if residual is not None:
         ld_r = _fp8_out(residual, "residual", dt, (rows, cols), dev)
-        h = empty((rows, cols), dtype=dt, device=dev) if h_out is None else h_out
-        ld_h = cols if h_out is None else _fp8_out(h, "h_out", dt, (rows, cols), dev)
+        if h_out is None:
+            h, ld_h = empty((rows, cols), dtype=dt, device=dev), cols
+        else:
+            h, ld_h = h_out, _fp8_out(h_out, "h_out", dt, (rows, cols), dev)
         hp = h.data_ptr()
     elif h_out is not None:
         raise ValueError("h_out needs a residual")

@@ -54,7 +54,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QArgs a, int lg, uin
 
 // Weights: one workgroup per 128 x 128 block, 16 lanes across and 16 rows at
 // a time, the whole block in registers (64 values a thread), so the input is
-// read once.  Bound by memory: 28672 x 8192 bf16 in 144 us, 4.9 TB/s, the rate
+// read once.  Bound by memory: 28672 x 8192 bf16 in 142 us, 5.0 TB/s, the rate
 // of a large copy; the fp64 quotients (about twelve instructions a value) hide
 // behind it.
 template <int DT>
@@ -111,7 +111,9 @@ struct NArgs {
 // y because codes next to a border of e4m3 would change with fp32's rounding
 // (the fp64 rate of gfx950 is that of unpacked fp32, and the kernel is bound
 // by memory: 16384 x 4096 bf16 with a residual in 100 us, 4.7 TB/s, against
-// 4.9 of a large copy; one row in 3.7 us).
+// 4.9 of a large copy; one row in 3.7 us; 333 x 8190 fp16, y too, in 11: a row
+// is one workgroup's chain of load, sum and about 500 fp64 instructions a wave,
+// and 77 of 256 CUs have two).
 template <int DT, int GDT, int NT, int P>
 __global__ __launch_bounds__(NT) void rmsnorm_kernel(NArgs a) {
   typedef typename Elem<DT>::type T;
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NArgs a) {
     }
     // columns past the row are zeros, but with rstd = NaN or inf they are NaN:
     // then so is the row
-    if (a.Y) {
+    if (a.Y) {   // rounded by way of fp32: off by at most half a step and 2^-25
       T f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = Elem<DT>::down((float)y[j]);

@@ -301,14 +301,14 @@ def test_gated(M, N, K, act, dtype):
         assert np.all(np.abs(v * e - ref) <= tol), how
 
 
-def test_products_take_any_stride_and_leave_the_rest():
+@pytest.mark.parametrize("M,N,K", [(70, 150, 400), (5, 150, 400), (30, 40, 401), (300, 600, 130), (3, 20, 9)])
+def test_products_take_any_stride_and_leave_the_rest(M, N, K):
     torch = torch_mod()
-    M, N, K = 70, 150, 400
     a, b, u = _matrix(M, K, 1, 1), _matrix(N, K, 128, 2, 0.05), _matrix(N, K, 128, 3, 0.05)
     want, wq = gq().fp8_gemm(a, b), gq().fp8_gated_gemm(a, b, u)
     F = gq().Fp8Matrix
     E4 = torch.float8_e4m3fn
-    for ld, off in [(401, 0), (416, 3), (512, 16)]:
+    for ld, off in [(K + 1, 0), ((K + 31) // 16 * 16, 3), (512, 16)]:
         s = lambda m: F(_strided(m.codes.view(torch.uint8), ld, off).view(E4), m.scales, m.block_rows)
         for aa, bb, uu in [(s(a), b, u), (a, s(b), s(u)), (s(a), s(b), s(u))]:
             wide = torch.full((M, N + 9), 7.0, dtype=torch.bfloat16, device="cuda")
