@@ -112,10 +112,22 @@ __device__ __forceinline__ i32x4 piece16(const uint8_t* row, int64_t k, int64_t 
 }
 
 // ---------------------------------------------------------------- epilogues
+// Sigmoids by the hardware's exp2 and reciprocal: within |x| + 4 units in the
+// last place, of a value that e^-|x| makes small where |x| is large.
+__device__ __forceinline__ float over_one_plus_exp2(float x, float z) {   // x/(1 + 2^z)
+  return x * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z));
+}
 __device__ __forceinline__ float activate(float x, int act) {
-  if (act == GPTQ_ACT_SILU) return x / (1.f + expf(-x));
+  if (act == GPTQ_ACT_SILU) return over_one_plus_exp2(x, x * -1.44269504f);
   if (act == GPTQ_ACT_GELU) return 0.5f * x * erfcf(x * -0.70710678f);   // Φ(x) without cancellation
-  return x / (1.f + expf(-1.5957691f * (x + 0.044715f * x * x * x)));    // (1 + tanh z)/2 = 1/(1 + e^-2z)
+  return over_one_plus_exp2(x, -2.30220820f * (x + 0.044715f * x * x * x));   // (1 + tanh y)/2 = 1/(1 + e^-2y)
+}
+
+// Codes of four values of a block.  The values carry fp32's rounding already, so
+// the quotient is rounded to fp32 too and moves as few over a border (a quotient
+// in fp64 took 1487 us where this takes 1447, 2048 x 28672 x 8192 to codes).
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+  return e4m3_pack4(a * inv, b * inv, c * inv, d * inv);
 }
 
 // Four neighbouring values of a row, `n` of them present.
@@ -487,15 +499,12 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
 #pragma unroll
       for (int q = 0; q < BN / WN; ++q) u = max(u, top[q * BM + ml]);
       const float s = e4m3_scale((double)__builtin_bit_cast(float, u));
-      const double sd = (double)s, inv = e4m3_inverse(s);
+      const float inv = 1.f / s;
       if (ml >= mleft) continue;
       if (wn == 0 && lane < 16) a.sc[(m0 + ml) * a.nb + bn] = s;
 #pragma unroll
       for (int j = 0; j < NO; ++j) {
-        float q[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) q[r] = e4m3_quotient((double)acc[j][i][r], sd, inv);
-        const uint32_t c = e4m3_pack4(q[0], q[1], q[2], q[3]);
+        const uint32_t c = codes4(acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3], inv);
         uint8_t* o = a.codes + (m0 + ml) * a.ld_codes + n0 + nl + j * 16;
         const int n = nleft - nl - j * 16;
         if (n >= 4) {
@@ -702,11 +711,18 @@ __global__ __launch_bounds__(256) void join_kernel(GArgs a, int splits) {
   for (int b = 0; b < NB; ++b) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[b][i] = 0.f;
-    for (int s = 0; s < splits; ++s) {
-      float v[8];
-      load8<GPTQ_F32>(a.P + (((int64_t)s * NB + b) * a.M + m) * a.N + n, c, v);
+    // four splits' loads in flight: 322 x 448 x 8960 in 12 splits 17.3 -> 15.2 us
+    for (int s = 0; s < splits; s += 4) {
+      float v[4][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[b][i] += v[i];
+      for (int u = 0; u < 4; ++u)
+        load8<GPTQ_F32>(a.P + (((int64_t)min(s + u, splits - 1) * NB + b) * a.M + m) * a.N + n, c, v[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (s + u < splits) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[b][i] += v[u][i];
+        }
     }
   }
   if constexpr (GATED) {
@@ -718,12 +734,9 @@ __global__ __launch_bounds__(256) void join_kernel(GArgs a, int splits) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) u = max(u, mag_bits(h[0][i]));
     const float s = e4m3_scale((double)__builtin_bit_cast(float, row16_max_u32(u)));
-    const double sd = (double)s, inv = e4m3_inverse(s);
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = e4m3_quotient((double)h[0][i], sd, inv);
-    store_codes8(a.codes + m * a.ld_codes + n, c, e4m3_pack4(q[0], q[1], q[2], q[3]),
-                 e4m3_pack4(q[4], q[5], q[6], q[7]));
+    const float inv = 1.f / s;
+    store_codes8(a.codes + m * a.ld_codes + n, c, codes4(h[0][0], h[0][1], h[0][2], h[0][3], inv),
+                 codes4(h[0][4], h[0][5], h[0][6], h[0][7], inv));
     if (lane == 0) a.sc[m * a.nb + blk] = s;
   } else {
     if (a.c_dt == GPTQ_F32) store8<GPTQ_F32>(static_cast<float*>(a.C) + m * a.ldc + n, c, h[0]);
