@@ -747,26 +747,30 @@ __global__ __launch_bounds__(256) void join_kernel(GArgs a, int splits) {
 
 // ---------------------------------------------------------------- choice and launch
 // The kernel for a product is the one that this model says is quickest.  Its
-// times are microseconds measured on MI355X at K = 4096 (fp8 instructions /
-// exact form): a stage of a tile with one workgroup on each of the 256 CUs,
-// and with as many as fit; launches with more take proportionally longer.
-// Small tiles win where there are few (512 x 4096: 64-tiles 18.7 / 29.1 us,
-// 128-tiles in two splits 25.2 / 31.3, 256-tiles in eight 39 / 45), large ones
-// where there are many (4096 x 4096: 131 / 201, 83 / 140, 67 / 118).
-struct TileCost { int bm, bn, fit; double one[2], full[2]; };   // [0] fp8, [1] exact
+// times are microseconds on MI355X (fp8 instructions / exact form): a stage of a
+// tile with one workgroup on each of the 256 CUs, and with as many as fit; a
+// round's start and epilogue.  Fitted to every kernel and split of 240 products
+// of random sizes (M to 2900, K to 10 944): what it picks takes 0.7 % longer
+// than the quickest on average, a third longer at worst (40 x 5760 x 1216: few
+// rows 6.3, 32-tiles 6.9, and the other way round near it).  Small tiles win
+// where there are few (512 x 4096: 64-tiles 18.7 / 29.1 us, 128-tiles in two
+// splits 25.2 / 31.3, 256-tiles in eight 39 / 45), large ones where there are
+// many (4096 x 4096: 131 / 201, 83 / 140, 67 / 118).
+struct TileCost { int bm, bn, fit; double one[2], full[2], ends; };   // [0] fp8, [1] exact
 constexpr TileCost kTiles[] = {
-    {32, 64, 3, {0.25, 0.45}, {0.50, 0.85}},
-    {64, 64, 2, {0.35, 0.62}, {0.46, 0.78}},
-    {128, 128, 2, {0.79, 1.16}, {1.20, 2.11}},
-    {256, 256, 1, {1.98, 3.57}, {1.98, 3.57}},
+    {32, 64, 3, {0.29, 0.44}, {0.53, 0.73}, 1.25},
+    {64, 64, 2, {0.36, 0.64}, {0.51, 0.81}, 1.45},
+    {128, 128, 2, {0.70, 1.13}, {1.14, 1.81}, 2.1},
+    {256, 256, 1, {1.77, 3.45}, {1.77, 3.45}, 2.3},
 };
 constexpr int kTileKinds = 4;
-constexpr double kLaunch = 4.0, kJoin = 3.5, kJoinBytes = 4.5e6;   // us, us, bytes per us
+// us, us, us for each four splits' loads, bytes per us
+constexpr double kLaunch = 2.7, kJoin = 2.2, kJoinLoads = 0.5, kJoinBytes = 4.0e6;
 // Few rows, the same way: a workgroup's start and end, its copies at the rate
 // one CU takes them (KB a us), or its waves' instructions (two waves a SIMD;
 // cycles a block and wave: conversions, products, the rest), or all weights
 // from memory (KB a us).
-constexpr double kFewLaunch = 2.3, kFewGroup = 1.0, kFewCopies = 75.0, kFewWeights = 7e3, kClock = 2100.0;
+constexpr double kFewLaunch = 1.8, kFewGroup = 1.3, kFewCopies = 81.0, kFewWeights = 7e3, kClock = 2100.0;
 
 struct Plan { int tile; int splits, kper; };   // tile -1: few rows
 
@@ -783,7 +787,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool exact, bool codes
     const int64_t groups = ceil_div(N, 16);
     const int fit = nb + mt == 2 ? 2 : 1, here = (int)std::min<int64_t>(fit, ceil_div(groups, 256));
     const double copied = 2.0 * kb * (nb + (M <= 8 ? 0.5 : mt)) / kFewCopies;
-    const double cycles = exact ? 1.25 * (64 * (nb + mt) + 80 * nb * mt + 150) : 48 * nb * mt + 200;
+    const double cycles = exact ? 92 * (nb + mt) + 115 * nb * mt + 65 : 48 * nb * mt + 200;
     const double issued = 2.0 * (double)ceil_div(kb, waves) * cycles / kClock;
     least = kFewLaunch + (codes ? kJoin : 0) +
             std::max((double)ceil_div(groups, 256 * here) * (kFewGroup + here * std::max(copied, issued)),
@@ -799,11 +803,13 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool exact, bool codes
       if (s > 1 && (!ws || tiles * s > 1024 || 2 * s > kb)) break;
       const int kper = ((int)kb + s - 1) / s, splits = ((int)kb + kper - 1) / kper;
       const int64_t load = (tiles * splits + 255) >> 8;   // workgroups of a CU
-      const double stage = load <= 1 ? c.one[e]
-                           : load < c.fit ? c.one[e] + (c.full[e] - c.one[e]) * (load - 1) / (c.fit - 1)
-                                          : c.full[e] * load / c.fit;
-      double t = kLaunch + stage * kper;
-      if (s > 1 || join) t += kJoin + (double)(s > 1 ? splits * nb : 1) * M * N * 8 / kJoinBytes;
+      const int64_t rest = load % c.fit;                  // those of its last round, if not full
+      double stage = (double)(load / c.fit) * c.full[e];
+      if (rest) stage += c.one[e] + (rest > 1 ? (c.full[e] - c.one[e]) * (double)(rest - 1) / (c.fit - 1) : 0);
+      double t = kLaunch + stage * kper + c.ends * (double)ceil_div(load, c.fit);
+      if (splits > 1 || join)
+        t += kJoin + (splits > 1 ? kJoinLoads * nb * (double)ceil_div(splits, 4) : 0) +
+             (double)(splits > 1 ? splits * nb : 1) * M * N * 8 / kJoinBytes;
       if (t < least) {
         least = t;
         best = {i, splits, kper};

@@ -223,7 +223,9 @@ SHAPES = [(*s, ["f32", "bf16", "f16"][i % 3]) for i, s in enumerate(SHAPES)] + [
     (480, 129, 1958, "f32"), (385, 7173, 211, "bf16"), (301, 6540, 200, "f32"), (66, 2803, 6309, "f16"),
     (65, 1350, 5633, "f32"), (1951, 6168, 203, "f16"), (131, 5510, 7906, "f32"), (3216, 1423, 7218, "bf16"),
     (20, 17000, 300, "bf16"), (47, 2000, 640, "bf16"), (16, 130, 65536, "bf16"), (49, 130, 65530, "f32"),
-    (65, 128, 1291, "f32"), (20, 300, 700, "f32"), (8, 1000, 2000, "f16"), (9, 1000, 2000, "f32")]
+    (65, 128, 1291, "f32"), (20, 300, 700, "f32"), (8, 1000, 2000, "f16"), (9, 1000, 2000, "f32"),
+    (33, 8324, 557, "bf16"), (1431, 30, 4875, "f16"), (65, 5740, 4516, "bf16"), (33, 30, 133, "f32"),
+    (197, 6989, 137, "f32"), (1098, 66, 5606, "f32"), (65, 5671, 3143, "f32"), (471, 8371, 5355, "f32")]
 
 
 @pytest.mark.parametrize("M,N,K,dtype", SHAPES)
@@ -260,7 +262,10 @@ GATED = [(*s, ["f32", "bf16", "f16"][i % 3]) for i, s in enumerate(GATED)] + [
     (1282, 4452, 203, "silu", "bf16"), (135, 2942, 7038, "gelu", "f32"), (456, 4178, 6348, "silu", "bf16"),
     (20, 9000, 300, "gelu", "bf16"), (65, 120, 2194, "silu", "bf16"), (65, 121, 1484, "silu", "f32"),
     (396, 4716, 4274, "silu", "f32"), (166, 5484, 258, "gelu_tanh", "f32"), (20, 300, 700, "silu", "f32"),
-    (40, 300, 700, "silu", "f32"), (8, 1000, 2000, "silu", "f32"), (64, 1000, 2000, "silu", "f32")]
+    (40, 300, 700, "silu", "f32"), (8, 1000, 2000, "silu", "f32"), (64, 1000, 2000, "silu", "f32"),
+    (17, 30, 136, "silu", "bf16"), (521, 36, 6938, "gelu", "f16"), (98, 6156, 137, "silu", "f32"),
+    (1421, 68, 4327, "gelu_tanh", "f32"), (66, 2769, 3937, "silu", "f32"), (169, 8277, 5581, "silu", "f32"),
+    (49, 32, 132, "gelu", "bf16")]
 
 
 @pytest.mark.parametrize("M,N,K,act,dtype", GATED)
