@@ -411,6 +411,7 @@ int gptq_w4a16_gemm(const void* A, int a_dtype, int64_t M, int64_t K, int64_t ld
 
 /* Quantize X into a block-scaled matrix.
  *  X           [rows x cols] of x_dtype, row stride ld_x >= cols.
+ *              rows <= 2^24, cols <= 65536, rows·cols <= 2^34 (also below).
  *  block_rows  1 (activations) or 128 (weights).
  *  codes, scales   out, as above; must not overlap X. */
 int gptq_fp8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,

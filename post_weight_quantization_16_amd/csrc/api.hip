@@ -124,6 +124,15 @@ int check_fp8_shape(int64_t rows, int64_t cols, const char* rn, const char* cn) 
     return fail(GPTQ_ERR_INVALID_ARG, "%s must be in [1, %lld]", cn, (long long)kMaxDin);
   return GPTQ_OK;
 }
+// ... of the calls that launch by rows and columns: with up to 2^34 elements
+// their grids stay below 2^32 threads at every shape.
+int check_fp8_size(int64_t rows, int64_t cols) {
+  const int rc = check_fp8_shape(rows, cols, "rows", "cols");
+  if (rc) return rc;
+  if (rows * cols > (int64_t(1) << 34))
+    return fail(GPTQ_ERR_INVALID_ARG, "rows * cols must be at most 2^34 (got %lld)", (long long)(rows * cols));
+  return GPTQ_OK;
+}
 // Element pointers must be aligned to their type (the calls that take any
 // byte address say so).
 bool misaligned(const void* p, int dt) { return (uintptr_t)p % (dt == GPTQ_F32 ? 4 : 2) != 0; }
@@ -528,7 +537,7 @@ int gptq_w4a16_gemm(const void* A, int a_dtype, int64_t M, int64_t K, int64_t ld
 int gptq_fp8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
                       int block_rows, uint8_t* codes, int64_t ld_codes, float* scales,
                       gptq_stream stream) {
-  int rc = check_fp8_shape(rows, cols, "rows", "cols");
+  int rc = check_fp8_size(rows, cols);
   if (rc) return rc;
   if (!valid_dtype(x_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown x_dtype %d", x_dtype);
   if (block_rows != 1 && block_rows != 128)
@@ -550,7 +559,7 @@ int gptq_rmsnorm_fp8(const void* X, int64_t ld_x, const void* R, int64_t ld_r, i
                      const void* gamma, int g_dtype, int64_t rows, int64_t cols, float eps,
                      void* H, int64_t ld_h, void* Y, int64_t ld_y, uint8_t* codes,
                      int64_t ld_codes, float* scales, gptq_stream stream) {
-  int rc = check_fp8_shape(rows, cols, "rows", "cols");
+  int rc = check_fp8_size(rows, cols);
   if (rc) return rc;
   if (!valid_dtype(x_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown x_dtype %d", x_dtype);
   if (g_dtype != x_dtype && g_dtype != GPTQ_F32)

@@ -126,6 +126,14 @@ def test_gated_refusals():
     assert call(A=None, G=None, U=None, c=None, s=None, M=0) == n.OK
 
 
+def test_element_calls_refuse_more_than_a_grid_takes():
+    for rows, cols in [(1 << 24, 1025), ((1 << 18) + 1, 65536)]:
+        assert n.lib().gptq_fp8_quantize(FAKE, n.BF16, rows, cols, cols, 1, FAKE, cols, FAKE, None) == n.ERR_INVALID_ARG
+        assert n.lib().gptq_rmsnorm_fp8(FAKE, cols, None, 0, n.BF16, FAKE, n.BF16, rows, cols, 1e-5, None, 0, None, 0,
+                                        FAKE, cols, FAKE, None) == n.ERR_INVALID_ARG
+        assert "2^34" in n.last_error()
+
+
 # ---------------------------------------------------------------- binding
 def _m(rows, cols, br, dtype=E4):
     return g.Fp8Matrix(torch.zeros(rows, cols, dtype=torch.uint8).view(dtype),
