@@ -156,7 +156,7 @@ __device__ __forceinline__ uint32_t mag_bits(float x) {
 // GHz that the power budget leaves.  The stages' copies out of L2 (64 KB a stage and
 // CU, 9 TB/s in all) and the LDS reads beside them set the pace: without the
 // copies it runs at 2.87, without the reads at 2.84 PFLOP/s.  The exact form
-// (2048 x 28672 x 8192 gated to codes: 1.48 ms, 1.30 PFLOP/s) is at 0.93 of
+// (2048 x 28672 x 8192 gated to codes: 1.44 ms, 1.34 PFLOP/s) is at 0.95 of
 // the rate that a large bf16 product reaches here; half its time is issue of
 // the conversions and adds beside the products.
 // BM x BN tile of C per workgroup, waves of WM x WN, K in stages of one block
@@ -529,7 +529,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
 // this reaches 75).  The waves' sums are added in wave order.
 // Bound: the weights' bytes, and at more than 16 rows the copies of A beside
 // them.  28672 x 8192 at 16 rows: 34 us, 6.8 TB/s out of the memory-side
-// cache; 11008 x 4096 gate and up at 4 rows, from memory: 19 us, 4.7 TB/s;
+// cache; 11008 x 4096 gate and up at 4 rows, from memory: 18 us, 5.0 TB/s;
 // 37 x 4000 x 11008 to fp32: 12.4 us.
 // NA: 8-row copies of A.
 constexpr int kFewRows = 64, kFewDepth = 2;
