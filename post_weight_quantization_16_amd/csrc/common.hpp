@@ -41,6 +41,31 @@ __device__ __forceinline__ void group_qparams(float mn, float mx, float amax, in
     z = fminf(fmaxf(rintf(-mn / s), 0.f), (float)maxq);
   }
 }
+
+// ---------------------------------------------------------------- memory -> LDS
+// A wave's copy from memory straight into LDS, no registers between: each lane
+// copies 16 (or 4) bytes from its address to lds + 16 (or 4)·lane, `lds` the
+// same in every lane.  Nothing but the caller's own s_waitcnt vmcnt orders a
+// copy before the reads of what it wrote: that is what inline asm is for here
+// (for the builtin the compiler waits for every copy before each LDS read).
+// The load takes its LDS address from M0, and gfx9 asks for one wait state
+// between a scalar write of M0 and the load that uses it; the compiler adds it
+// for the builtin but does not look into an asm, so the s_nop is part of it,
+// and M0 is declared as changed.
+__device__ __forceinline__ void lds_copy16(unsigned lds, const void* a) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(lds), "v"(a) : "m0", "memory");
+}
+// The same from base + offset, the base the same in every lane.
+__device__ __forceinline__ void lds_copy16(unsigned lds, const void* base, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(lds), "v"(offset), "s"(base) : "m0", "memory");
+}
+__device__ __forceinline__ void lds_copy4(unsigned lds, const void* a) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :: "s"(lds), "v"(a) : "m0", "memory");
+}
+
 inline size_t align_up(size_t x, size_t a = 256) { return (x + a - 1) / a * a; }
 
 // ---------------------------------------------------------------- fp32 GEMM

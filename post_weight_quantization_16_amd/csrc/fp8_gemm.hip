@@ -273,8 +273,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
       if (idx < BM / 8) p = a.sa + (m0 + min(idx * 8 + r, mleft - 1)) * a.kb;
       else if (GATED) p = (r == 0 ? a.sb[0] : a.sb[NB - 1]) + n0 / 128 * a.kb;
       else p = a.sb[0] + min(n0 / 128 + min(r, 1), a.nb - 1) * a.kb;
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
-                   :: "s"(sbase + T::SCALES + (unsigned)((g & 1) * T::SCB + idx * 256)), "v"(p + k) : "memory");
+      lds_copy4(sbase + T::SCALES + (unsigned)((g & 1) * T::SCB + idx * 256), p + k);
     }
   };
   // copies i0 .. i1 - 1 of a stage (through registers: all of them with the first)
@@ -286,12 +285,9 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
 #pragma unroll
       for (int i = i0; i < i1; ++i) {
         const int seg = w * T::PER + i;
-        // 16 bytes per lane to LDS M0 + 16·lane; no register result, ordered
-        // before the reads by the stage barriers
-        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
-                     :: "s"(sbase + buf + (unsigned)seg * 1024u), "v"(KEEP ? voff[KEEP ? i : 0] : (uint32_t)seg_offset(seg, l)),
-                        "s"(seg_base(seg) + (int64_t)(kbeg + st) * 128)
-                     : "memory");
+        // ordered before the reads by the stage barriers
+        lds_copy16(sbase + buf + (unsigned)seg * 1024u, seg_base(seg) + (int64_t)(kbeg + st) * 128,
+                   KEEP ? voff[KEEP ? i : 0] : (uint32_t)seg_offset(seg, l));
       }
     } else if (i0 == 0) {
       // rows that end inside this block, or start at odd addresses: through
@@ -582,10 +578,7 @@ __global__ __launch_bounds__((Few<NA, GATED>::WAVES * 64)) void few_rows_kernel(
     if (kbeg + j < last_wide) {
 #pragma unroll
       for (int i = 0; i < F::PER; ++i)
-        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
-                     :: "s"(rbase + (unsigned)dest(slot, i)), "v"(voff[i]),
-                        "s"(base(i) + (int64_t)(kbeg + j) * 128)
-                     : "memory");
+        lds_copy16(rbase + (unsigned)dest(slot, i), base(i) + (int64_t)(kbeg + j) * 128, voff[i]);
     } else {
       i32x4 v[F::PER];
 #pragma unroll
@@ -605,9 +598,7 @@ __global__ __launch_bounds__((Few<NA, GATED>::WAVES * 64)) void few_rows_kernel(
     for (int i = 0; i < 2 * MT + 1; ++i) {
       const float* p = i < 2 * MT ? a.sa + (int64_t)min(i * 8 + r, mleft - 1) * a.kb
                                   : (r == 0 ? a.sb[0] : a.sb[NB - 1]) + n0 / 128 * a.kb;
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
-                   :: "s"(rbase + (unsigned)(kFewDepth * F::SLOT + (g & 1) * F::SCB + i * 256)), "v"(p + k)
-                   : "memory");
+      lds_copy4(rbase + (unsigned)(kFewDepth * F::SLOT + (g & 1) * F::SCB + i * 256), p + k);
     }
   };
 

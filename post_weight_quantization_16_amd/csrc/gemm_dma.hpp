@@ -112,10 +112,8 @@ struct OpCopy {
 #pragma unroll
     for (int j = 0; j < NWI; ++j) {
       const char* a = src[j] + (int64_t)st * step;
-      // 16 bytes per lane from a to LDS M0 + 16·lane; no register result,
       // ordered before the reads by the stage waits
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
-                   :: "s"(lds + (unsigned)(w * NWI + j) * 1024u), "v"(a) : "memory");
+      lds_copy16(lds + (unsigned)(w * NWI + j) * 1024u, a);
     }
   }
 };

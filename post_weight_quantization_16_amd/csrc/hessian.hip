@@ -409,11 +409,7 @@ __global__ __launch_bounds__(256) void syrk256_kernel(const uint16_t* __restrict
     const unsigned lb = sbase + (unsigned)((st % NBUF) * FSTAGE) + (unsigned)(w * NI + i) * 1024u;
     const bool ok = colok[i] && rrow[i] < rem;
     const char* a = ok ? pbase[i] + soff : reinterpret_cast<const char*>(zero16);
-    // global_load_lds_dwordx4: 16 bytes per lane from address a to LDS
-    // M0 + 16·lane.  It has no register result; the stage's wait
-    // (s_waitcnt vmcnt) is what orders it before the reads.
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
-                 :: "s"(lb), "v"(a) : "memory");
+    lds_copy16(lb, a);   // the stage's wait (s_waitcnt vmcnt) orders it before the reads
   };
   auto dma = [&](int st) {
 #pragma unroll

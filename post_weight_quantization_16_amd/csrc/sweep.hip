@@ -186,10 +186,7 @@ __global__ __launch_bounds__(256) void sweep_kernel(SweepArgs a) {
     for (int seg = wave; seg < kBlock * kBlock / 256; seg += nthr >> 6) {
       const int e = seg * 256 + lane * 4, i = e / kBlock, j = e % kBlock;
       const float* src = a.Ublk + (int64_t)i * a.ldu + j;
-      // 16 bytes per lane to LDS M0 + 16·lane; no register result, waited
-      // for by the vmcnt wait below
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
-                   :: "s"(sbase + (unsigned)seg * 1024u), "v"(src) : "memory");
+      lds_copy16(sbase + (unsigned)seg * 1024u, src);   // waited for by the vmcnt wait below
     }
   } else {
     for (int e0 = t * 4; e0 < kBlock * kBlock; e0 += nthr * 4 * 16) {
