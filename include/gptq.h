@@ -98,7 +98,9 @@ enum { GPTQ_WS_HESSIAN = 0, GPTQ_WS_PREPARE = 1, GPTQ_WS_QUANTIZE = 2, GPTQ_WS_O
  * NULL for the Hessian.  GPTQ_WS_LAYER is one job of
  * gptq_quantize_independent (its Hessian, preparation and quantization).
  * For GPTQ_WS_W4A16, GPTQ_WS_FP8_GEMM and GPTQ_WS_FP8_GATED the shape is
- * d_out = N, d_in = K, n_tok = M (p unused).
+ * d_out = N, d_in = K, n_tok = M (p unused); of the two FP8 kinds, 256 says
+ * that no call of this shape uses a workspace (NULL does as well), and a size
+ * that one uses is 512 or more.
  * Returns 0 for invalid arguments.  Workspaces need 256-byte alignment
  * (every hipMalloc'd pointer has it). */
 size_t gptq_workspace_bytes(int which, int64_t d_out, int64_t d_in, int64_t n_tok,

@@ -688,7 +688,7 @@ def rmsnorm_fp8(X, gamma, eps: float = 1e-6, residual=None, want_q: bool = True,
 
 def _fp8_workspace(which, M, N, K, ws, dev):
     """(address, bytes, tensor to keep) of the split-K workspace; sizes that
-    need none get none."""
+    need none (the library says 256) get none."""
     if ws is None:
         need = _native.lib().gptq_workspace_bytes(which, N, K, M, None)
         if need <= 256:

@@ -887,14 +887,15 @@ template <bool GATED> hipError_t run_dt(GArgs& a, void* ws, hipStream_t s) {
   }
 }
 
-// enough for every output form
+// enough for every output form; 256, which no real need rounds up to, if none
+// uses a workspace
 size_t ws_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
-  size_t most = 256;
+  size_t most = 0;
   for (int form = 0; form < (gated ? 3 : 2); ++form) {   // 16 bits, fp32, codes
     const Plan p = plan_of(M, N, K, gated, form > 0, form == 2, true);
     most = std::max(most, plan_bytes(p, M, N, gated, form == 2));
   }
-  return align_up(most);
+  return most ? std::max<size_t>(512, align_up(most)) : 256;
 }
 
 }  // namespace

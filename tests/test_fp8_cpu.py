@@ -178,3 +178,12 @@ def test_binding_refusals():
                                  (A, B, B, dict(out=torch.zeros(4, 32)), "shape")]:
         with pytest.raises(ValueError, match=match):
             g.fp8_gated_gemm(a, gt, up, **kw)
+
+
+def test_a_size_that_uses_a_workspace_asks_for_more_than_one_that_does_not():
+    """256 bytes mean that NULL does as well.  Codes of a few rows go through
+    the workspace as fp32, however few they are."""
+    need = n.lib().gptq_workspace_bytes
+    for M, N, K in [(1, 64, 8192), (1, 1, 4096), (2, 32, 4096), (64, 1, 2048)]:
+        assert need(n.WS_FP8_GATED, N, K, M, None) > 256, (M, N, K)
+    assert need(n.WS_FP8_GEMM, 64, 256, 4, None) == 256

@@ -498,3 +498,16 @@ def test_offsets_past_32_bits():
     s = gq().rmsnorm_fp8(x[-200:], torch.ones(cols, device="cuda"), 1e-6)
     assert torch.equal(n.q.scales[-200:], s.q.scales)
     assert torch.equal(n.q.codes[-200:].view(torch.uint8), s.q.codes.view(torch.uint8))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 64, 8192), (2, 32, 4096), (16, 4, 2000)])
+def test_codes_of_the_smallest_products_get_their_workspace(M, N, K):
+    """The binding's own workspace and a caller's give the same bits, also
+    where 256 bytes would hold the whole result."""
+    torch = torch_mod()
+    n = gq()._native
+    a, g_, u = _matrix(M, K, 1, 1), _matrix(N, K, 128, 2, 0.05), _matrix(N, K, 128, 3, 0.05)
+    ws = torch.empty(n.lib().gptq_workspace_bytes(n.WS_FP8_GATED, N, K, M, None), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 256
+    x, y = gq().fp8_gated_gemm(a, g_, u), gq().fp8_gated_gemm(a, g_, u, ws=ws)
+    assert torch.equal(x.scales, y.scales) and np.array_equal(_codes(x), _codes(y))
