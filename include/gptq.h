@@ -426,7 +426,8 @@ int gptq_fp8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, in
  *  X, R       [rows x cols] of x_dtype, row strides ld_x, ld_r >= cols; R may
  *             be NULL.
  *  gamma      [cols] of g_dtype: x_dtype or GPTQ_F32.
- *  eps        finite, >= 0 (with 0, a row of zeros gives NaN: 0/0).
+ *  eps        finite, >= 0, taken as given, in fp64 (with 0, a row of zeros
+ *             gives NaN: 0/0).
  *  H          out [rows x cols] of x_dtype, row stride ld_h: the sum that the
  *             next residual addition takes; may be NULL; may be X or R itself
  *             (same address and stride), else must not overlap them.
@@ -436,7 +437,7 @@ int gptq_fp8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, in
  *             together with Y.
  * The sum of squares and y are formed in fp64. */
 int gptq_rmsnorm_fp8(const void* X, int64_t ld_x, const void* R, int64_t ld_r, int x_dtype,
-                     const void* gamma, int g_dtype, int64_t rows, int64_t cols, float eps,
+                     const void* gamma, int g_dtype, int64_t rows, int64_t cols, double eps,
                      void* H, int64_t ld_h, void* Y, int64_t ld_y, uint8_t* codes,
                      int64_t ld_codes, float* scales, gptq_stream stream);
 

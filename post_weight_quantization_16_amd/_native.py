@@ -156,7 +156,7 @@ def lib() -> ctypes.CDLL:
     L.gptq_fp8_quantize.argtypes = [_vp, _int, _i64, _i64, _i64, _int, _vp, _i64, _vp, _vp]
     L.gptq_fp8_quantize.restype = _int
     L.gptq_rmsnorm_fp8.argtypes = [_vp, _i64, _vp, _i64, _int, _vp, _int, _i64, _i64,
-                                   ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp]
+                                   ctypes.c_double, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp]
     L.gptq_rmsnorm_fp8.restype = _int
     L.gptq_fp8_gemm.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _int, _i64,
                                 _vp, _sz, _vp]

@@ -556,7 +556,7 @@ int gptq_fp8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, in
 }
 
 int gptq_rmsnorm_fp8(const void* X, int64_t ld_x, const void* R, int64_t ld_r, int x_dtype,
-                     const void* gamma, int g_dtype, int64_t rows, int64_t cols, float eps,
+                     const void* gamma, int g_dtype, int64_t rows, int64_t cols, double eps,
                      void* H, int64_t ld_h, void* Y, int64_t ld_y, uint8_t* codes,
                      int64_t ld_codes, float* scales, gptq_stream stream) {
   int rc = check_fp8_size(rows, cols);
@@ -564,7 +564,7 @@ int gptq_rmsnorm_fp8(const void* X, int64_t ld_x, const void* R, int64_t ld_r, i
   if (!valid_dtype(x_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown x_dtype %d", x_dtype);
   if (g_dtype != x_dtype && g_dtype != GPTQ_F32)
     return fail(GPTQ_ERR_INVALID_ARG, "g_dtype must be x_dtype or GPTQ_F32");
-  if (!(eps >= 0.f) || !std::isfinite(eps))
+  if (!(eps >= 0.0) || !std::isfinite(eps))
     return fail(GPTQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
   if (ld_x < cols || (R && ld_r < cols) || (H && ld_h < cols) || (Y && ld_y < cols) ||
       (codes && ld_codes < cols))

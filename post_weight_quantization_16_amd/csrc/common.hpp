@@ -188,7 +188,7 @@ hipError_t fp8_quantize_launch(const void* X, int dt, int64_t rows, int64_t cols
                                int block_rows, uint8_t* codes, int64_t ld_c, float* scales,
                                hipStream_t s);
 hipError_t rmsnorm_fp8_launch(const void* X, int64_t ld_x, const void* R, int64_t ld_r, int dt,
-                              const void* gamma, int g_dt, int64_t rows, int64_t cols, float eps,
+                              const void* gamma, int g_dt, int64_t rows, int64_t cols, double eps,
                               void* S, int64_t ld_s, void* Y, int64_t ld_y, uint8_t* codes,
                               int64_t ld_c, float* scales, hipStream_t s);
 size_t fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);

@@ -264,10 +264,10 @@ hipError_t fp8_quantize_launch(const void* X, int dt, int64_t rows, int64_t cols
 }
 
 hipError_t rmsnorm_fp8_launch(const void* X, int64_t ld_x, const void* R, int64_t ld_r, int dt,
-                              const void* gamma, int g_dt, int64_t rows, int64_t cols, float eps,
+                              const void* gamma, int g_dt, int64_t rows, int64_t cols, double eps,
                               void* S, int64_t ld_s, void* Y, int64_t ld_y, uint8_t* codes,
                               int64_t ld_c, float* scales, hipStream_t s) {
-  const NArgs a{X, ld_x, R, ld_r, gamma, rows, cols, 1.0 / (double)cols, (double)eps, S, ld_s, Y, ld_y, codes, ld_c, scales,
+  const NArgs a{X, ld_x, R, ld_r, gamma, rows, cols, 1.0 / (double)cols, eps, S, ld_s, Y, ld_y, codes, ld_c, scales,
                 ceil_div(cols, kFp8Block)};
   if (dt == GPTQ_F32) return launch_rmsnorm<GPTQ_F32, GPTQ_F32>(a, s);
   if (dt == GPTQ_BF16)

@@ -511,3 +511,22 @@ def test_codes_of_the_smallest_products_get_their_workspace(M, N, K):
     assert ws.numel() > 256
     x, y = gq().fp8_gated_gemm(a, g_, u), gq().fp8_gated_gemm(a, g_, u, ws=ws)
     assert torch.equal(x.scales, y.scales) and np.array_equal(_codes(x), _codes(y))
+
+
+@pytest.mark.parametrize("eps", [1e-5, 1e-6, 3e-12])
+def test_rmsnorm_rows_far_below_eps(eps):
+    """eps counts in full: rows whose mean square is small beside it are
+    x/sqrt(eps), rounded once, which eps in fp32 (up to 2^-25 off) would not
+    give."""
+    torch = torch_mod()
+    x = torch.randn(16, 1000, generator=torch.Generator().manual_seed(3)).cuda()
+    x *= (eps ** 0.5 * 2.0 ** -torch.arange(4, 20, device="cuda"))[:, None].float()
+    gamma = torch.ones(1000, device="cuda")
+    out = gq().rmsnorm_fp8(x, gamma, eps, want_y=True)
+    ref = fp8.rmsnorm(_np(x), _np(gamma), eps)
+    assert np.all(np.abs(_np(out.y) - ref) <= np.abs(ref) * HALF["f32"] * (1 + 2.0 ** -12))
+    _, s = fp8.quantize(ref, 1)
+    got = out.q.scales.cpu().numpy()
+    # fp64 errors (below 2^-48) can move a scale over a border of fp32 in one of 2^23
+    assert np.sum(got != s) <= 1 and np.all(np.abs(got / s.astype(np.float64) - 1) <= 2.0 ** -23)
+    _same_codes(fp8.decode(_codes(out.q)), ref / fp8.expand(got, 1, 16, 1000), "codes")
