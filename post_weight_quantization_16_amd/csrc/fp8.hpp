@@ -13,12 +13,9 @@
 
 namespace gq {
 
-typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
-typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(8))) int i32x8;
 
 constexpr int kFp8Block = 128;        // columns of a block (and rows, for weights)
-constexpr float kE4m3Max = 448.f;
 
 // Scale of a block from its largest magnitude (NaN or infinite: NaN).  For an
 // fp32 amax the product with 1/448 rounds to fp32 as the quotient does: amax/7
@@ -55,11 +52,7 @@ __device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float 
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
 }
 
-// Maximum over the 16 lanes of a DPP row (every lane gets it).
-template <int CTRL> __device__ __forceinline__ float dpp_f(float x) {
-  const int v = __builtin_bit_cast(int, x);
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false));
-}
+// Another lane's value, by a DPP control.
 template <int CTRL> __device__ __forceinline__ double dpp_d(double x) {
   const uint64_t b = __builtin_bit_cast(uint64_t, x);
   const int lo = (int)(uint32_t)b, hi = (int)(uint32_t)(b >> 32);
@@ -69,6 +62,7 @@ template <int CTRL> __device__ __forceinline__ double dpp_d(double x) {
 }
 // row_ror:n rotates inside each row of 16 lanes
 constexpr int kRor8 = 0x128, kRor4 = 0x124, kRor2 = 0x122, kRor1 = 0x121;
+// Maximum over the 16 lanes of a DPP row (every lane gets it).
 __device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, kRor8, 0xF, 0xF, false));
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, kRor4, 0xF, 0xF, false));

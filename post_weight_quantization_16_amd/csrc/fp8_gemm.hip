@@ -427,20 +427,22 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
 
   const int nl = wn * WC + 4 * (lane >> 4);   // this lane's first column in the tile
   if constexpr (EPI == kPartial) {
-    if (GATED && a.kper >= a.kb) {   // unsplit: h itself
+    if constexpr (GATED && !FAST && BC < 128) {   // codes of a tile below a block: here unsplit too
+      if (a.kper >= a.kb) {   // h itself
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int ml = wm * WM + i * 16 + l15;
+        for (int i = 0; i < MI; ++i) {
+          const int ml = wm * WM + i * 16 + l15;
 #pragma unroll
-        for (int j = 0; j < NI / NB; ++j) {
+          for (int j = 0; j < NI / NB; ++j) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[j][i][r] = activate(acc[j][i][r], a.act) * acc[NI / NB + j][i][r];
-          if (ml < mleft)
-            put4<GPTQ_F32>(a.P, (m0 + ml) * a.N + n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+            for (int r = 0; r < 4; ++r)
+              acc[j][i][r] = activate(acc[j][i][r], a.act) * acc[NI / NB + j][i][r];
+            if (ml < mleft)
+              put4<GPTQ_F32>(a.P, (m0 + ml) * a.N + n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+          }
         }
+        return;
       }
-      return;
     }
     float* P = a.P + (int64_t)split * NB * a.M * a.N;
 #pragma unroll
