@@ -530,3 +530,55 @@ def test_rmsnorm_rows_far_below_eps(eps):
     # fp64 errors (below 2^-48) can move a scale over a border of fp32 in one of 2^23
     assert np.sum(got != s) <= 1 and np.all(np.abs(got / s.astype(np.float64) - 1) <= 2.0 ** -23)
     _same_codes(fp8.decode(_codes(out.q)), ref / fp8.expand(got, 1, 16, 1000), "codes")
+
+
+# ---------------------------------------------------------------- exact sums
+def _integers(rows, cols, br, seed, shift=0):
+    """Codes -7..7 and scales 2^-shift and half of it: products of two such
+    matrices are multiples of 2^-2 (times the shifts) below 2^24 of them for
+    every K <= 65536, so all sums are exact in fp32 in any order, and an eight
+    of products spans less than 2^13, so the fp8 instruction drops nothing."""
+    torch = torch_mod()
+    rng = np.random.default_rng(seed)
+    v = rng.integers(-7, 8, (rows, cols)).astype(np.float32)
+    s = 2.0 ** -(shift + rng.integers(0, 2, (-(-rows // br), -(-cols // 128))))
+    codes = torch.zeros(rows, (cols + 15) // 16 * 16, dtype=torch.float8_e4m3fn, device="cuda")
+    codes[:, :cols] = torch.from_numpy(v).cuda().to(torch.float8_e4m3fn)
+    return gq().Fp8Matrix(codes[:, :cols], torch.from_numpy(s.astype(np.float32)).cuda(), br)
+
+
+@pytest.mark.parametrize("M,N,K", sorted({s[:3] for s in SHAPES}))
+def test_gemm_of_integers_is_exact(M, N, K):
+    """Every type, every kernel and split: the exact result, rounded once.  A
+    column of K that is left out, taken twice or scaled wrongly shows."""
+    torch = torch_mod()
+    a, b = _integers(M, K, 1, 1), _integers(N, K, 128, 2)
+    ref = torch.from_numpy(fp8.values(_values(a), 1) @ fp8.values(_values(b), 128).T)
+    n = gq()._native
+    for dtype, code in [("f32", n.F32), ("bf16", n.BF16), ("f16", n.F16)]:
+        want = ref.to(_t(dtype)).cuda()
+        assert torch.equal(gq().fp8_gemm(a, b, out_dtype=_t(dtype)), want), dtype
+        D = torch.full_like(want, float("nan"))
+        rc = n.lib().gptq_fp8_gemm(a.codes.data_ptr(), a.scales.data_ptr(), M, K, (K + 15) // 16 * 16,
+                                   b.codes.data_ptr(), b.scales.data_ptr(), N, (K + 15) // 16 * 16,
+                                   D.data_ptr(), code, N, None, 0, torch.cuda.current_stream().cuda_stream)
+        assert rc == n.OK and torch.equal(D, want), f"{dtype} unsplit"
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (16, 130, 65536), (37, 300, 11008), (66, 2803, 6309), (480, 129, 1958),
+                                   (301, 6540, 200), (65, 5740, 4516), (300, 4096, 640)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gemm_16_bits_is_as_near_as_its_instruction_allows(M, N, K, dtype):
+    """Beside the output's rounding, no value is further off than eight
+    spreads of what the instruction drops, and the whole no further than one
+    (a rounding's mean square is a third of its largest)."""
+    a, b = _matrix(M, K, 1, 1), _matrix(N, K, 128, 2, 0.05)
+    ref, mag = fp8.matmul(_values(a), _values(b))
+    acc, sigma = fp8.accumulation_bound(mag, K), fp8.dropped_spread(_values(a), _values(b))
+    C = gq().fp8_gemm(a, b, out_dtype=_t(dtype))
+    _check(C, ref, acc + 8 * sigma, dtype, f"GEMM {(M, N, K)} {dtype} tight")
+    err = np.linalg.norm(_np(C) - ref)
+    limit = np.sqrt(np.sum(sigma ** 2 + (np.abs(ref) * HALF[dtype]) ** 2 / 3)) + np.linalg.norm(acc)
+    log(f"GEMM {(M, N, K)} {dtype}: error norm {err / np.linalg.norm(ref):.3e} of the result's, limit "
+        f"{limit / np.linalg.norm(ref):.3e}, spread {np.linalg.norm(sigma) / np.linalg.norm(ref):.3e}")
+    assert err <= limit
