@@ -475,10 +475,13 @@ int gptq_fp8_gemm(const uint8_t* A, const float* a_scales, int64_t M, int64_t K,
  *  activation          a gptq_activation.
  *  C, c_dtype, ldc     out [M x N] of c_dtype: h rounded, or NULL;
  *  codes, ld_codes, scales   out: h block-scaled in 1 x 128 blocks (what the
- *                      next gptq_fp8_gemm takes as A), or NULL.  h and
- *                      its quotients by the scale are fp32, so a code is the
- *                      nearest but for values within 2^-22 of a border.  One
- *                      of the two outputs must be given, not both.
+ *                      next gptq_fp8_gemm takes as A), or NULL.  h and its
+ *                      quotients by the scale are fp32: the scale is that of
+ *                      the computed h, and a code the nearest to the computed
+ *                      h over it but for quotients within 2^-22 of a border.
+ *                      Beside exact sums h has fp32's error, and about one
+ *                      code in 10^5 is the border's other side.  One of the
+ *                      two outputs must be given, not both.
  *  ws                  as for gptq_fp8_gemm, of GPTQ_WS_FP8_GATED. */
 int gptq_fp8_gated_gemm(const uint8_t* A, const float* a_scales, int64_t M, int64_t K, int64_t lda,
                         const uint8_t* G, const float* g_scales, int64_t ldg, const uint8_t* U,

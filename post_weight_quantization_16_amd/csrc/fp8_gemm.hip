@@ -117,8 +117,10 @@ __device__ __forceinline__ i32x4 piece16(const uint8_t* row, int64_t k, int64_t 
 }
 
 // ---------------------------------------------------------------- epilogues
-// Sigmoids by the hardware's exp2 and reciprocal: within |x| + 4 units in the
-// last place, of a value that e^-|x| makes small where |x| is large.
+// Sigmoids by the hardware's exp2 and reciprocal.  What counts is the rounding
+// of the exponent: silu is within |x| + 4 units of 2^-23, gelu_tanh, whose
+// exponent is 1.6x + 0.07x³ after three roundings, within 2.5|x| + |x|³/9 + 4
+// (15 at -3, 81 at -8), of values that e^-|x| makes small there.
 __device__ __forceinline__ float over_one_plus_exp2(float x, float z) {   // x/(1 + 2^z)
   return x * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z));
 }
@@ -128,11 +130,12 @@ __device__ __forceinline__ float activate(float x, int act) {
   return over_one_plus_exp2(x, -2.30220820f * (x + 0.044715f * x * x * x));   // (1 + tanh y)/2 = 1/(1 + e^-2y)
 }
 
-// Codes of four values of a block.  The values and the block's largest, its
-// scale, carry fp32's rounding already; one more in the quotient moves no more
-// codes over a border (1024 x 8192 x 2048: 50 of 8.4 million differ from those
-// of exact sums, 49 with quotients in fp64, which took 1487 us where this takes
-// 1447, 2048 x 28672 x 8192 to codes).
+// Codes of four values of a block.  1/s and the product round by 2^-24 each, so
+// a code is that of the fp32 value over its scale but within 2^-22 of a border.
+// The values and the block's largest, its scale, carry fp32's rounding already;
+// one more in the quotient moves no more codes over a border (1024 x 8192 x
+// 2048: 50 of 8.4 million differ from those of exact sums, 49 with quotients in
+// fp64, which took 1487 us where this takes 1447, 2048 x 28672 x 8192 to codes).
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
   return e4m3_pack4(a * inv, b * inv, c * inv, d * inv);
 }

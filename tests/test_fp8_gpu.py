@@ -582,3 +582,84 @@ def test_gemm_16_bits_is_as_near_as_its_instruction_allows(M, N, K, dtype):
     log(f"GEMM {(M, N, K)} {dtype}: error norm {err / np.linalg.norm(ref):.3e} of the result's, limit "
         f"{limit / np.linalg.norm(ref):.3e}, spread {np.linalg.norm(sigma) / np.linalg.norm(ref):.3e}")
     assert err <= limit
+
+
+# ---------------------------------------------------------------- codes of gated products
+def _gated_null(a, g_, u, act, q):
+    """Codes without a workspace."""
+    torch = torch_mod()
+    n = gq()._native
+    (M, K), N = a.codes.shape, g_.codes.shape[0]
+    ld = (K + 15) // 16 * 16
+    rc = n.lib().gptq_fp8_gated_gemm(
+        a.codes.data_ptr(), a.scales.data_ptr(), M, K, ld, g_.codes.data_ptr(), g_.scales.data_ptr(), ld,
+        u.codes.data_ptr(), u.scales.data_ptr(), ld, N, {"silu": 0, "gelu": 1, "gelu_tanh": 2}[act], None, 0, 0,
+        q.codes.data_ptr(), q.codes.stride(0) if M > 1 else (N + 15) // 16 * 16, q.scales.data_ptr(), None, 0,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == n.OK, n.last_error()
+
+
+@pytest.mark.parametrize("M,N,K,act", sorted({s[:4] for s in GATED}))
+def test_gated_of_integers(M, N, K, act):
+    """With exact sums (gate values of about 2) h depends on neither kernel
+    nor split.  fp32: the activation's own error alone.  Codes, with and
+    without a workspace: scales of the computed h bit for bit, codes nearest
+    to it but within 2^-22 of a border (1/s and the product round by 2^-24
+    each).  16 bits: the product act·(A·Uᵀ) rounded once, to fp32 first or not
+    (one instruction rounds a product of two floats straight to
+    fp16).  With p that product, h is within 2^-24·|p| of it and the result
+    within a half step of p or of h, so within a half step and 2·2^-24·|p| of
+    h; 2·2^-24 is at most 2^-12 of fp16's half step 2^-11, and |p| at most
+    |h|·(1 + 2^-23)."""
+    torch = torch_mod()
+    k = max(0, round(float(np.log2(14 * K ** 0.5))) - 1)
+    a, g_, u = _integers(M, K, 1, 1), _integers(N, K, 128, 2, k), _integers(N, K, 128, 3, k)
+    x = fp8.values(_values(a), 1)
+    cg, cu = x @ fp8.values(_values(g_), 128).T, x @ fp8.values(_values(u), 128).T
+    f = fp8.activation(cg, act)
+    # the exponent of gelu_tanh, rounded before exp: |x| + |x|³/8 units more
+    z = np.minimum(np.abs(cg) + np.abs(cg) ** 3 / 8, 100.0)
+    h = gq().fp8_gated_gemm(a, g_, u, act, out_dtype=torch.float32)
+    err = np.abs(_np(h) - f * cu)
+    assert np.all(err <= np.abs(f * cu) * 2.0 ** -24 * (10 + 4 * z) + 1e-37 * (1 + np.abs(cu)))
+    q1 = gq().fp8_gated_gemm(a, g_, u, act)
+    q2 = gq().Fp8Matrix(torch.zeros_like(q1.codes), torch.zeros_like(q1.scales), 1)
+    _gated_null(a, g_, u, act, q2)
+    _, s = fp8.quantize(_np(h), 1)
+    for q, how in [(q1, "workspace"), (q2, "none")]:
+        assert np.array_equal(q.scales.cpu().numpy(), s), how
+        _same_codes(fp8.decode(_codes(q)), _np(h) / fp8.expand(s, 1, M, N), how)
+    for dtype in ("bf16", "f16"):
+        C = gq().fp8_gated_gemm(a, g_, u, act, out_dtype=_t(dtype))
+        assert np.all(np.abs(_np(C) - _np(h)) <= np.abs(_np(h)) * HALF[dtype] * (1 + 2.0 ** -11) + TINY[dtype] * HALF[dtype]), dtype
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 1000, 2000), (64, 1000, 2000), (67, 1421, 3204), (300, 2050, 512), (1025, 900, 520)])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_gated_codes_beside_exact_sums(M, N, K, act):
+    """On inputs with cancellation, through few rows, tiles, splits and with
+    no workspace: a code differs from that of the exact sums only where a
+    border lies within the error bound of the fp32 sums, and few do: with h
+    off by 2^-20 of itself, a border is within reach of one in 2^15 values
+    (steps are at least 1/16 of a value), given twice that for cancellation."""
+    torch = torch_mod()
+    a, g_, u = _matrix(M, K, 1, 1), _matrix(N, K, 128, 2, 0.05), _matrix(N, K, 128, 3, 0.05)
+    ref, bound = fp8.gated(_values(a), _values(g_), _values(u), act)
+    v, s = fp8.quantize(ref, 1)
+    e = fp8.expand(s, 1, M, N)
+    q1 = gq().fp8_gated_gemm(a, g_, u, act)
+    q2 = gq().Fp8Matrix(torch.zeros_like(q1.codes), torch.zeros_like(q1.scales), 1)
+    _gated_null(a, g_, u, act, q2)
+    for q, how in [(q1, "workspace"), (q2, "none")]:
+        got = fp8.decode(_codes(q))
+        bad = got != v
+        x = np.abs(ref[bad] / e[bad])
+        far = fp8.border_distance(x) * np.maximum(x, 2.0 ** -10)
+        # the scale's own error moves every quotient of its block
+        top = np.pad(np.abs(ref), ((0, 0), (0, -N % 128))).reshape(M, -1, 128)
+        ts = np.pad(bound, ((0, 0), (0, -N % 128))).reshape(M, -1, 128)
+        ds = np.repeat(np.max(ts, 2) / np.max(top, 2), 128, 1)[:, :N]
+        assert np.all(far <= bound[bad] / e[bad] + x * (ds[bad] + 2.0 ** -21)), how
+        log(f"GATED {(M, N, K)} {act} codes, {how}: {bad.sum()} of {bad.size} beside a border, "
+            f"scales differing {np.mean(q.scales.cpu().numpy() != s):.3f}")
+        assert bad.sum() <= 2.0 ** -14 * bad.size + 4, how
