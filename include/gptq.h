@@ -408,8 +408,8 @@ int gptq_w4a16_gemm(const void* A, int a_dtype, int64_t M, int64_t K, int64_t ld
  *  codes, so that what is computed from it is NaN.
  * rows (or M) == 0 is a no-op in every call: the tensors of that side may be
  * NULL.  Outputs must not overlap inputs or each other unless a call says so.
- * All calls are asynchronous, return argument errors and GPTQ_ERR_HIP
- * only, and give the same bits on every run. */
+ * All calls are asynchronous, return argument errors (GPTQ_ERR_WORKSPACE
+ * among them) and GPTQ_ERR_HIP only, and give the same bits on every run. */
 
 /* Quantize X into a block-scaled matrix.
  *  X           [rows x cols] of x_dtype, row stride ld_x >= cols.
@@ -431,7 +431,8 @@ int gptq_fp8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, in
  *  H          out [rows x cols] of x_dtype, row stride ld_h: the sum that the
  *             next residual addition takes; may be NULL; may be X or R itself
  *             (same address and stride), else must not overlap them.
- *  Y          out [rows x cols] of x_dtype, row stride ld_y: y rounded; may be
+ *  Y          out [rows x cols] of x_dtype, row stride ld_y: y rounded (to 16
+ *             bits by way of fp32: within half a step and 2^-25 of it); may be
  *             NULL; must not overlap an input.
  *  codes, scales   out, y block-scaled; both or neither NULL, and not NULL
  *             together with Y.
@@ -482,7 +483,10 @@ int gptq_fp8_gemm(const uint8_t* A, const float* a_scales, int64_t M, int64_t K,
  *                      Beside exact sums h has fp32's error, and about one
  *                      code in 10^5 is the border's other side.  One of the
  *                      two outputs must be given, not both.
- *  ws                  as for gptq_fp8_gemm, of GPTQ_WS_FP8_GATED. */
+ *  ws                  as for gptq_fp8_gemm, of GPTQ_WS_FP8_GATED.  With NULL,
+ *                      codes come from 256-row tiles over all of K whatever
+ *                      M is: right, but for few rows many times slower (one
+ *                      row, K = 8192: about 220 us in place of 20). */
 int gptq_fp8_gated_gemm(const uint8_t* A, const float* a_scales, int64_t M, int64_t K, int64_t lda,
                         const uint8_t* G, const float* g_scales, int64_t ldg, const uint8_t* U,
                         const float* u_scales, int64_t ldu, int64_t N, int activation, void* C,

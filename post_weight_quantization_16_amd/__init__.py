@@ -701,7 +701,10 @@ def _fp8_workspace(which, M, N, K, ws, dev):
 
 def fp8_gemm(A: Fp8Matrix, B: Fp8Matrix, out_dtype=None, out=None, ws=None):
     """C = A·Bᵀ: A [M, K] with block_rows 1, B [N, K] with block_rows 128,
-    C [M, N] in out_dtype (bfloat16 unless given, or `out`'s type).
+    C [M, N] in out_dtype (bfloat16 unless given, or `out`'s type).  float32
+    has exact products and fp32 sums; the 16-bit types take the fp8 matrix
+    instruction, twice as fast, whose sums are off by 1.5e-5 to 6e-5 of the
+    result's norm (values whose sum cancels: by more than their own rounding).
     ws: the split-K workspace (allocated here when None; pass one to reuse)."""
     M, K, lda, dev = _fp8_arg(A, "A", 1)
     N, kb, ldb, _ = _fp8_arg(B, "B", FP8_BLOCK, dev)

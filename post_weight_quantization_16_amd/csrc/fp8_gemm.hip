@@ -15,7 +15,9 @@
 //   fast   one v_mfma_f32_16x16x128_f8f6f4.  It aligns every eight
 //          neighbouring products to the power of two of the largest, cuts the
 //          others (toward zero) below 2^-13 of it, and adds the eights in
-//          fp32.  Measured, an error of 1.5e-5 of the result's norm on normal
+//          fp32 (the powers of two are those of the factors, 2^-6 for a
+//          subnormal code, so beside one of these it cuts up to 2^3 higher).
+//          Measured, an error of 1.5e-5 of the result's norm on normal
 //          data and 3e-5 to 6e-5 where one column in fifty is an outlier.
 //          Taken where C has 16 bits: beside the norm of C's own rounding
 //          (fp16 2.1e-4, bf16 1.7e-3) that adds 1 to 4 % and nothing.  It is
@@ -161,14 +163,14 @@ __device__ __forceinline__ uint32_t mag_bits(float x) {
 }
 
 // ---------------------------------------------------------------- tile kernel
-// Bound: at 4096 x 28672 x 8192 to bf16 (fp8 instructions, 256 x 256 tiles) 850
-// us, 2.26 PFLOP/s; the matrix cores are busy 55 % of the cycles, at the 1.7
-// GHz that the power budget leaves.  The stages' copies out of L2 (64 KB a stage and
-// CU, 9 TB/s in all) and the LDS reads beside them set the pace: without the
-// copies it runs at 2.87, without the reads at 2.84 PFLOP/s.  The exact form
-// (2048 x 28672 x 8192 gated to codes: 1.44 ms, 1.34 PFLOP/s) is at 0.95 of
-// the rate that a large bf16 product reaches here; half its time is issue of
-// the conversions and adds beside the products.
+// Bound: 4096 x 28672 x 8192 to bf16 (fp8 instructions, 256 x 256 tiles) takes
+// 0.84 to 0.90 ms by the machine, 2.14 to 2.28 PFLOP/s; the matrix cores are
+// busy 55 % of the cycles, the LDS and the vector units 35 % each, at the 1.7
+// GHz that the power budget leaves; the stages' copies out of L2 (64 KB a stage
+// and CU, 9 TB/s in all) run beside them.  The exact form (2048 x 28672 x 8192
+// gated to codes: 1.44 to 1.52 ms, 1.27 to 1.33 PFLOP/s) is at 0.90 to 0.95 of
+// the rate that a large bf16 product reaches here; the issue of its conversions
+// and adds takes 46 % of the cycles, the products 55 %.
 // BM x BN tile of C per workgroup, waves of WM x WN, K in stages of one block
 // in a ring of NS stage buffers.  Stages go from memory straight into LDS
 // (global_load_lds: no registers, no LDS store instructions), NS-1 ahead.
@@ -537,8 +539,9 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
 // this reaches 75).  The waves' sums are added in wave order.
 // Bound: the weights' bytes, and at more than 16 rows the copies of A beside
 // them.  28672 x 8192 at 16 rows: 34 us, 6.8 TB/s out of the memory-side
-// cache; 11008 x 4096 gate and up at 4 rows, from memory: 18 us, 5.0 TB/s;
-// 37 x 4000 x 11008 to fp32: 12.4 us.
+// cache.  Kernel times with the weights there / from memory: 11008 x 4096 gate
+// and up at 4 rows 18.6 / 21.4 us (4.2 TB/s), 4096 x 4096 at one row 5.5 / 6.0,
+// 37 x 4000 x 11008 to fp32 13.9 / 16.8.
 // NA: 8-row copies of A.
 constexpr int kFewRows = 64, kFewDepth = 2;
 
@@ -755,7 +758,7 @@ __global__ __launch_bounds__(256) void join_kernel(GArgs a, int splits) {
 // round's start and epilogue.  Fitted to every kernel and split of 240 products
 // of random sizes (M to 2900, K to 10 944): what it picks takes 0.7 % longer
 // than the quickest on average, a third longer at worst (40 x 5760 x 1216: few
-// rows 6.3, 32-tiles 6.9, and the other way round near it).  Small tiles win
+// rows 10.0, 32-tiles 7.3).  Small tiles win
 // where there are few (512 x 4096: 64-tiles 18.7 / 29.1 us, 128-tiles in two
 // splits 25.2 / 31.3, 256-tiles in eight 39 / 45), large ones where there are
 // many (4096 x 4096: 131 / 201, 83 / 140, 67 / 118).

@@ -29,7 +29,7 @@ __device__ __forceinline__ void encode8(const float (&v)[8], float s, uint32_t& 
 
 // Activations: 16 lanes per 1 x 128 block, eight columns a lane.  A workgroup
 // of 256 threads takes 2^lg blocks of a row side by side and 16 >> lg rows.
-// Bound by memory: 517 x 11008 fp16 in 6.5 us (2.6 TB/s, mostly the launch's
+// Bound by memory: 517 x 11008 fp16 in 6.8 us (2.5 TB/s, mostly the launch's
 // ramp), 1 x 4096 in 2.0 us (a launch).
 template <int DT>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QArgs a, int lg, uint32_t chunks) {
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QArgs a, int lg, uin
 
 // Weights: one workgroup per 128 x 128 block, 16 lanes across and 16 rows at
 // a time, the whole block in registers (64 values a thread), so the input is
-// read once.  Bound by memory: 28672 x 8192 bf16 in 139 us, 5.1 TB/s, the rate
+// read once.  Bound by memory: 28672 x 8192 bf16 in 137 to 139 us, 5.1 TB/s, the rate
 // of a large copy; the fp64 quotients (about twelve instructions a value) hide
 // behind it.
 template <int DT>
@@ -109,11 +109,12 @@ struct NArgs {
 // ... (P of them, eight columns each), so 16 neighbouring lanes hold a block.
 // The sum of squares, 1/sqrt and y are fp64: the sum because rows are long,
 // y because codes next to a border of e4m3 would change with fp32's rounding
-// (the fp64 rate of gfx950 is that of unpacked fp32, and the kernel is bound
-// by memory: 16384 x 4096 bf16 with a residual in 100 us, 4.7 TB/s, against
-// 4.9 of a large copy; one row in 3.5 us; 333 x 8190 fp16, y too, in 11.6: a row
-// is one workgroup's chain of load, sum and about 500 fp64 instructions a wave,
-// and 77 of 256 CUs have two).
+// (the fp64 rate of gfx950 is that of unpacked fp32).  Many rows are bound by
+// memory: 16384 x 4096 bf16 with a residual in 99 us, 4.8 TB/s, against 4.9 of
+// a large copy.  A few hundred are not: 333 x 8190 fp16, y too, takes 11.8, four
+// times its bytes' time, since a row is one workgroup's chain of load, sum and
+// about 500 fp64 instructions a wave, with nothing to hide it (77 of 256 CUs
+// have two rows).  One row takes 3.8 us.
 template <int DT, int GDT, int NT, int P>
 __global__ __launch_bounds__(NT) void rmsnorm_kernel(NArgs a) {
   typedef typename Elem<DT>::type T;
