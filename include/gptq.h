@@ -431,8 +431,7 @@ int gptq_fp8_quantize(const void* X, int x_dtype, int64_t rows, int64_t cols, in
  *  H          out [rows x cols] of x_dtype, row stride ld_h: the sum that the
  *             next residual addition takes; may be NULL; may be X or R itself
  *             (same address and stride), else must not overlap them.
- *  Y          out [rows x cols] of x_dtype, row stride ld_y: y rounded (to 16
- *             bits by way of fp32: within half a step and 2^-25 of it); may be
+ *  Y          out [rows x cols] of x_dtype, row stride ld_y: y rounded; may be
  *             NULL; must not overlap an input.
  *  codes, scales   out, y block-scaled; both or neither NULL, and not NULL
  *             together with Y.

@@ -32,17 +32,21 @@ __device__ __forceinline__ double e4m3_inverse(float s) {
   return __builtin_fma(__builtin_fma(-sd, r, 1.0), r, r);
 }
 
-// x/s as a float that rounds to e4m3 as the exact quotient does: the quotient
-// in fp64 (one correction by the exact remainder, so ties stay ties), its last
-// 32 bits folded into a sticky bit above them, which leaves a value fp32 holds
-// exactly and keeps the side of every border.  fp32 alone would move about one
-// code in 10^6 over a border.
-__device__ __forceinline__ float e4m3_quotient(double x, double s, double inv) {
-  double q = x * inv;
-  q = __builtin_fma(__builtin_fma(-q, s, x), inv, q);
-  uint64_t b = __builtin_bit_cast(uint64_t, q);
+// x as a float that rounds to 16 bits or fewer as x does: its last 32 bits
+// folded into a sticky bit above them, which leaves 21 bits, a value fp32 holds
+// exactly (from 2^-126 up), and keeps the side of every border.
+__device__ __forceinline__ float sticky_float(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
   const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32) | (lo < 1u ? lo : 1u);
   return (float)__builtin_bit_cast(double, (uint64_t)hi << 32);
+}
+
+// x/s as a float that rounds to e4m3 as the exact quotient does: the quotient
+// in fp64, with one correction by the exact remainder, so ties stay ties.  fp32
+// alone would move about one code in 10^6 over a border.
+__device__ __forceinline__ float e4m3_quotient(double x, double s, double inv) {
+  double q = x * inv;
+  return sticky_float(__builtin_fma(__builtin_fma(-q, s, x), inv, q));
 }
 
 // Four floats to four e4m3 codes, byte i from argument i (round to nearest

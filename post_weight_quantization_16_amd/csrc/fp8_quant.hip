@@ -193,10 +193,10 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NArgs a) {
     }
     // columns past the row are zeros, but with rstd = NaN or inf they are NaN:
     // then so is the row
-    if (a.Y) {   // rounded by way of fp32: off by at most half a step and 2^-25
+    if (a.Y) {   // rounded once (bf16 below 2^-126: by way of fp32)
       T f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = Elem<DT>::down((float)y[j]);
+      for (int j = 0; j < 8; ++j) f[j] = Elem<DT>::down(DT == GPTQ_F32 ? (float)y[j] : sticky_float(y[j]));
       store8_raw<DT>(static_cast<T*>(a.Y) + row * a.ld_y + col(i), n, f);
     }
     if (!a.codes) continue;   // the whole grid alike

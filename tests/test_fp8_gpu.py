@@ -663,3 +663,24 @@ def test_gated_codes_beside_exact_sums(M, N, K, act):
         log(f"GATED {(M, N, K)} {act} codes, {how}: {bad.sum()} of {bad.size} beside a border, "
             f"scales differing {np.mean(q.scales.cpu().numpy() != s):.3f}")
         assert bad.sum() <= 2.0 ** -14 * bad.size + 4, how
+
+
+# ---------------------------------------------------------------- the norm's y
+def _rounded(x, dtype):
+    """x (fp64) to the nearest of a 16-bit type, ties to even, in one step."""
+    bits, low = {"bf16": (8, -126), "f16": (11, -14)}[dtype]
+    step = 2.0 ** (np.maximum(np.frexp(x)[1] - 1, low) + 1 - bits)   # of the value's binade
+    return np.rint(x / step) * step
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(333, 8190, "f16"), (300, 8192, "bf16"), (70, 40000, "f16")])
+def test_rmsnorm_y_is_rounded_once(rows, cols, dtype):
+    """Bit for bit the fp64 result's nearest: by way of fp32, one value in 2^14
+    (fp16) or 2^17 (bf16) would land on a border first and then on its wrong
+    side."""
+    torch = torch_mod()
+    x = _rand(rows, cols, 7, dtype)
+    gamma = (1 + 0.1 * torch.randn(cols, generator=torch.Generator().manual_seed(1))).cuda()
+    y = _np(gq().rmsnorm_fp8(x, gamma, 1e-5, want_q=False, want_y=True).y)
+    ref = _rounded(fp8.rmsnorm(_np(x), _np(gamma), 1e-5), dtype)
+    assert np.array_equal(y, ref), f"{np.sum(y != ref)} of {y.size} differ"
