@@ -485,7 +485,7 @@ int gptq_fp8_gemm(const uint8_t* A, const float* a_scales, int64_t M, int64_t K,
  *  ws                  as for gptq_fp8_gemm, of GPTQ_WS_FP8_GATED.  With NULL,
  *                      codes come from 256-row tiles over all of K whatever
  *                      M is: right, but for few rows many times slower (one
- *                      row, K = 8192: about 220 us in place of 20). */
+ *                      row, K = 8192, N = 64: 190 us in place of 13). */
 int gptq_fp8_gated_gemm(const uint8_t* A, const float* a_scales, int64_t M, int64_t K, int64_t lda,
                         const uint8_t* G, const float* g_scales, int64_t ldg, const uint8_t* U,
                         const float* u_scales, int64_t ldu, int64_t N, int activation, void* C,
