@@ -91,16 +91,19 @@ typedef void* gptq_stream;
 typedef enum { GPTQ_ACT_SILU = 0, GPTQ_ACT_GELU = 1, GPTQ_ACT_GELU_TANH = 2 } gptq_activation;
 
 enum { GPTQ_WS_HESSIAN = 0, GPTQ_WS_PREPARE = 1, GPTQ_WS_QUANTIZE = 2, GPTQ_WS_OBQ = 3,
-       GPTQ_WS_W4A16 = 4, GPTQ_WS_LAYER = 5, GPTQ_WS_FP8_GEMM = 6, GPTQ_WS_FP8_GATED = 7 };
+       GPTQ_WS_W4A16 = 4, GPTQ_WS_LAYER = 5, GPTQ_WS_FP8_GEMM = 6, GPTQ_WS_FP8_GATED = 7,
+       GPTQ_WS_FP8_LINEAR = 8,
+       /* gptq_expert_workspace_bytes: */
+       GPTQ_WS_MOE = 9, GPTQ_WS_EXPERT_GATED = 10, GPTQ_WS_EXPERT_GEMM = 11 };
 
 /* Workspace size in bytes that call `which` (GPTQ_WS_*) needs for the given
  * shape.  n_tok is used by the Hessian call and GPTQ_WS_LAYER only; p may be
  * NULL for the Hessian.  GPTQ_WS_LAYER is one job of
  * gptq_quantize_independent (its Hessian, preparation and quantization).
- * For GPTQ_WS_W4A16, GPTQ_WS_FP8_GEMM and GPTQ_WS_FP8_GATED the shape is
- * d_out = N, d_in = K, n_tok = M (p unused); of the two FP8 kinds, 256 says
- * that no call of this shape uses a workspace (NULL does as well), and a size
- * that one uses is 512 or more.
+ * For GPTQ_WS_W4A16, GPTQ_WS_FP8_GEMM, GPTQ_WS_FP8_GATED and
+ * GPTQ_WS_FP8_LINEAR the shape is d_out = N, d_in = K, n_tok = M (p unused);
+ * of the FP8 kinds, 256 says that no call of this shape uses a workspace (NULL
+ * does as well), and a size that one uses is 512 or more.
  * Returns 0 for invalid arguments.  Workspaces need 256-byte alignment
  * (every hipMalloc'd pointer has it). */
 size_t gptq_workspace_bytes(int which, int64_t d_out, int64_t d_in, int64_t n_tok,
@@ -491,6 +494,136 @@ int gptq_fp8_gated_gemm(const uint8_t* A, const float* a_scales, int64_t M, int6
                         const float* u_scales, int64_t ldu, int64_t N, int activation, void* C,
                         int c_dtype, int64_t ldc, uint8_t* codes, int64_t ld_codes, float* scales,
                         void* ws, size_t ws_bytes, gptq_stream stream);
+
+/* A linear layer with its epilogue in one kernel:
+ *   C = act(A·Bᵀ + bias) + residual, one rounding to C's type,
+ * or act(A·Bᵀ + bias) block-scaled (what the next product takes as A).  The
+ * products and sums are gptq_fp8_gemm's: exact with fp32 sums for GPTQ_F32 and
+ * for codes, the fp8 matrix instruction for the 16-bit types; bias, activation
+ * and residual are fp32.
+ *  A, a_scales         [M x K] activations, row stride lda.
+ *  B, b_scales         [N x K] weights, row stride ldb.
+ *  bias                [N] of bias_dtype, or NULL.
+ *  activation          a gptq_activation, or -1 for none.
+ *  R, ld_r             residual [M x N] of c_dtype, row stride ld_r >= N, or
+ *                      NULL; may be C itself (same address and stride), else
+ *                      must not overlap it.  Not with codes.
+ *  C, c_dtype, ldc     out [M x N] of c_dtype, or NULL;
+ *  codes, ld_codes, scales   out, 1 x 128 blocks, or NULL; rounded as those of
+ *                      gptq_fp8_gated_gemm.  One of the two outputs must be
+ *                      given, not both.
+ *  ws                  as for gptq_fp8_gemm, of GPTQ_WS_FP8_LINEAR. */
+int gptq_fp8_linear(const uint8_t* A, const float* a_scales, int64_t M, int64_t K, int64_t lda,
+                    const uint8_t* B, const float* b_scales, int64_t N, int64_t ldb,
+                    const void* bias, int bias_dtype, int activation, const void* R, int64_t ld_r,
+                    void* C, int c_dtype, int64_t ldc, uint8_t* codes, int64_t ld_codes,
+                    float* scales, void* ws, size_t ws_bytes, gptq_stream stream);
+
+/* ---- Experts in 8-bit floating point --------------------------------------
+ * A feed-forward block of which each token uses top_k of E sets of weights
+ * ("experts"): the router's choice, the gated projection of every token by its
+ * experts, and the product back, summed over a token's experts.
+ *
+ * A slot is a token's j-th expert, numbered t·top_k + j.  The products take
+ * the slots sorted by expert:
+ *  offsets  [E + 1] int32: expert e has the sorted positions offsets[e] ..
+ *           offsets[e+1] - 1; offsets[E] is the number of slots that have an
+ *           expert.
+ *  order    [T·top_k] int32: the slot at each position, ascending within an
+ *           expert; -1 from position offsets[E] on.
+ * The same expert may stand twice in a token's slots.  Tables that are not of
+ * this form give undefined outputs, but no access outside the operands.
+ * E <= 1024, top_k <= min(E, 64), T <= 2^24, T·top_k <= 2^30.  T == 0 is a
+ * no-op but for offsets, which become zeros. */
+
+/* Workspace of an experts' call: GPTQ_WS_MOE (gptq_moe_route, gptq_moe_plan; N
+ * and K unused), GPTQ_WS_EXPERT_GATED, GPTQ_WS_EXPERT_GEMM.  256 says that the
+ * call uses none (NULL does as well).  Returns 0 for invalid arguments. */
+size_t gptq_expert_workspace_bytes(int which, int64_t T, int64_t top_k, int64_t n_experts, int64_t N,
+                                   int64_t K);
+
+/* Scores of a router, for gptq_moe_route: softmax over the experts, or
+ * 1/(1 + e^-l) of each logit l. */
+typedef enum { GPTQ_SCORE_SOFTMAX = 0, GPTQ_SCORE_SIGMOID = 1 } gptq_scores;
+
+/* Choose each token's experts and their weights, and sort the slots:
+ *   p = the scores of the logits,  c = p + bias (the order is that of c;
+ *   without a bias that of the logits);
+ *   the experts in n_groups groups of E/n_groups neighbours, of which the
+ *   top_groups best are kept by the sum of their group_top (1 or 2) largest c
+ *   (those there are);
+ *   ids = the top_k experts of the kept groups with the largest c, in
+ *   descending order; weights = p of these, over their sum with renormalize
+ *   (equal ones where the sum is 0), times scale.
+ * Ties go to the lowest index, among groups too.  Scores, c and sums are fp64;
+ * a weight is rounded once.
+ *  logits     [T x E] of dtype, row stride ld >= E.  -inf excludes an expert,
+ *             and so does a bias of -inf; where fewer than top_k are left the
+ *             last ids are -1, with weight 0.  A row with a NaN (or, for
+ *             softmax, +inf; or a NaN bias) gets the ids 0, 1, .. and NaN
+ *             weights, so that the token's output is NaN.
+ *  bias       [E] fp32 or NULL.
+ *  mask       [T] bytes or NULL: a token with 0 (padding) gets the ids -1 and
+ *             weights 0, whatever its logits are.
+ *  n_groups   1..16, a divisor of E; top_k <= top_groups·E/n_groups.
+ *  scale      finite.
+ *  ids, weights   out [T x top_k] int32, fp32.
+ *  offsets, order out, as above, or both NULL.
+ *  ws         of GPTQ_WS_MOE.
+ * All calls of this section are asynchronous, return argument errors
+ * (GPTQ_ERR_WORKSPACE among them) and GPTQ_ERR_HIP only, and give the same
+ * bits on every run. */
+int gptq_moe_route(const void* logits, int dtype, int64_t T, int64_t n_experts, int64_t ld,
+                   const float* bias, const uint8_t* mask, int scores, int top_k, int n_groups,
+                   int top_groups, int group_top, int renormalize, double scale, int32_t* ids,
+                   float* weights, int32_t* offsets, int32_t* order, void* ws, size_t ws_bytes,
+                   gptq_stream stream);
+
+/* Sort the slots of ids [T x top_k] that were chosen elsewhere; an id below 0
+ * or from E on is a slot without an expert.  ws of GPTQ_WS_MOE. */
+int gptq_moe_plan(const int32_t* ids, int64_t T, int top_k, int64_t n_experts, int32_t* offsets,
+                  int32_t* order, void* ws, size_t ws_bytes, gptq_stream stream);
+
+/* The gated projection of each token by each of its experts:
+ *   h[i] = act(x[t]·G_eᵀ)·(x[t]·U_eᵀ)
+ * for the sorted positions i (expert e, token t).  Rows from offsets[E] on are
+ * left as they were.  Products, activation and codes as in
+ * gptq_fp8_gated_gemm: exact with fp32 sums for GPTQ_F32 and for codes.
+ *  A, a_scales      [T x K] activations, row stride lda.
+ *  G, g_scales, ldg, next_g   [E][N x K] gate weights: rows ldg bytes apart,
+ *                   experts next_g bytes (>= 0); scales dense, [E][ceil(N/128) x
+ *                   ceil(K/128)].  U, u_scales, ldu, next_u: up weights.
+ *  activation, C, c_dtype, ldc, codes, ld_codes, scales   as for
+ *                   gptq_fp8_gated_gemm, T·top_k rows.
+ *  ws               of GPTQ_WS_EXPERT_GATED. */
+int gptq_fp8_expert_gated_gemm(const uint8_t* A, const float* a_scales, int64_t T, int64_t K,
+                               int64_t lda, int top_k, const int32_t* offsets, const int32_t* order,
+                               int64_t n_experts, const uint8_t* G, const float* g_scales,
+                               int64_t ldg, int64_t next_g, const uint8_t* U, const float* u_scales,
+                               int64_t ldu, int64_t next_u, int64_t N, int activation, void* C,
+                               int c_dtype, int64_t ldc, uint8_t* codes, int64_t ld_codes,
+                               float* scales, void* ws, size_t ws_bytes, gptq_stream stream);
+
+/* The product back, summed over each token's experts:
+ *   y[t] = Σ_j weights[t,j]·(h[i(t,j)]·D_eᵀ) + residual[t], one rounding,
+ * i(t,j) the sorted position of slot t·top_k + j; slots without an expert add
+ * nothing.  Products as in gptq_fp8_gemm (exact with fp32 sums for GPTQ_F32);
+ * the sum over j is fp32, in the order of j.
+ *  H, h_scales      [T·top_k x K] activations by sorted position, row stride
+ *                   ldh; rows from offsets[E] on are not read.
+ *  ids, weights     [T x top_k]; offsets and order as gptq_moe_plan makes them
+ *                   of these ids.
+ *  D, d_scales, ldd, next_d   [E][N x K] weights.
+ *  R, ld_r          residual [T x N] of c_dtype or NULL; may be C itself (same
+ *                   address and stride), else must not overlap it.
+ *  C, c_dtype, ldc  out [T x N].
+ *  ws               of GPTQ_WS_EXPERT_GEMM; required where that is not 256. */
+int gptq_fp8_expert_gemm(const uint8_t* H, const float* h_scales, int64_t T, int64_t K, int64_t ldh,
+                         int top_k, const int32_t* ids, const float* weights, const int32_t* offsets,
+                         const int32_t* order, int64_t n_experts, const uint8_t* D,
+                         const float* d_scales, int64_t ldd, int64_t next_d, int64_t N,
+                         const void* R, int64_t ld_r, void* C, int c_dtype, int64_t ldc, void* ws,
+                         size_t ws_bytes, gptq_stream stream);
 
 /* Per-stage timing, for measurement only.  gptq_timing(1) clears what was
  * recorded and starts bracketing, on the caller's stream, the launches of

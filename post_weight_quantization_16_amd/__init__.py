@@ -12,7 +12,9 @@ memory and streams only).
     out = quantize_layer(W, prep, params)         # qweight, scales, zeros, ...
 
 8-bit floating point (block-scaled e4m3 matrices, Fp8Matrix): fp8_quantize,
-rmsnorm_fp8, fp8_gemm, fp8_gated_gemm.
+rmsnorm_fp8, fp8_gemm, fp8_linear (bias, activation, residual), fp8_gated_gemm;
+and for blocks of experts (Fp8Experts, Routing): moe_route, moe_plan,
+fp8_quantize_experts, fp8_expert_gated_gemm, fp8_expert_gemm.
 """
 from __future__ import annotations
 
@@ -27,6 +29,8 @@ __all__ = [
     "quantize_layer", "quantize", "workspace_bytes", "version", "Prepared", "Quantized",
     "Exported", "export", "quantize_layers", "obq_layer", "timing", "timing_read", "w4a16_gemm",
     "Fp8Matrix", "Normed", "fp8_quantize", "rmsnorm_fp8", "fp8_gemm", "fp8_gated_gemm",
+    "fp8_linear", "Fp8Experts", "Routing", "moe_route", "moe_plan", "fp8_quantize_experts",
+    "fp8_expert_gated_gemm", "fp8_expert_gemm", "expert_workspace_bytes",
 ]
 
 
@@ -765,6 +769,304 @@ def fp8_gated_gemm(A: Fp8Matrix, gate: Fp8Matrix, up: Fp8Matrix, activation: str
     _launch(dev, _native.lib().gptq_fp8_gated_gemm, A.codes.data_ptr(), A.scales.data_ptr(), M, K,
             lda, gate.codes.data_ptr(), gate.scales.data_ptr(), ldg, up.codes.data_ptr(),
             up.scales.data_ptr(), ldu, N, act, cp, cdt, ldc, qc, ldq, qs, wp, wn)
+    return out
+
+
+def fp8_linear(A: Fp8Matrix, B: Fp8Matrix, bias=None, activation: str | None = None, residual=None,
+               out_dtype=None, out=None, ws=None):
+    """act(A·Bᵀ + bias) + residual: A [M, K] with block_rows 1, B [N, K] with
+    block_rows 128, bias [N] (float32/bfloat16/float16), residual [M, N] of
+    the result's type.  Returns [M, N] in out_dtype (bfloat16 unless given, or
+    `out`'s type), rounded once; with out_dtype torch.float8_e4m3fn (or an
+    Fp8Matrix `out`) an Fp8Matrix with block_rows 1, without a residual.
+    Products and sums are fp8_gemm's; out may be residual itself.
+    ws: the split-K workspace (allocated here when None; pass one to reuse)."""
+    M, K, lda, dev = _fp8_arg(A, "A", 1)
+    N, kb, ldb, _ = _fp8_arg(B, "B", FP8_BLOCK, dev)
+    empty, e4m3 = _t8()[:2]
+    if kb != K:
+        raise ValueError(f"A has {K} columns, B has {kb}")
+    act = -1
+    if activation is not None:
+        act = _ACTIVATIONS.get(activation)
+        if act is None:
+            raise ValueError(f"activation must be None or one of {sorted(_ACTIVATIONS)} (got {activation!r})")
+    bp, bdt = None, 0
+    if bias is not None:
+        bdt = _fp8_dtype(bias, "bias")
+        if bias.shape != (N,) or not bias.is_contiguous() or bias.device != dev:
+            raise ValueError(f"bias must be contiguous of shape {(N,)} on {dev}")
+        bp = bias.data_ptr()
+    cp, cdt, ldc, qc, ldq, qs, rp, ldr = None, 0, 0, None, 0, None, None, 0
+    if isinstance(out, Fp8Matrix) or (out is None and out_dtype is e4m3):
+        if residual is not None:
+            raise ValueError("a residual needs a tensor result, not an Fp8Matrix")
+        if out is None:
+            out, ldq = _fp8_new(M, N, 1, dev)
+        else:
+            if out_dtype is not None and out_dtype is not e4m3:
+                raise ValueError(f"an Fp8Matrix out is {e4m3} (got {out_dtype})")
+            mo, no, ldq, _ = _fp8_arg(out, "out", 1, dev)
+            if (mo, no) != (M, N):
+                raise ValueError(f"out must have shape {(M, N)} (got {(mo, no)})")
+        qc, qs = out.codes.data_ptr(), out.scales.data_ptr()
+    else:
+        if out is None:
+            out = empty((M, N), dtype=out_dtype or _torch().bfloat16, device=dev)
+            ldc = N
+        else:
+            if out_dtype is not None and out.dtype != out_dtype:
+                raise ValueError(f"out must be {out_dtype} (got {out.dtype})")
+            ldc = _fp8_out(out, "out", out.dtype, (M, N), dev)
+        cdt = _fp8_dtype(out, "out")
+        cp = out.data_ptr()
+        if residual is not None:
+            ldr = _fp8_out(residual, "residual", out.dtype, (M, N), dev)
+            rp = residual.data_ptr()
+    wp, wn, ws = _fp8_workspace(_native.WS_FP8_LINEAR, M, N, K, ws, dev)
+    _launch(dev, _native.lib().gptq_fp8_linear, A.codes.data_ptr(), A.scales.data_ptr(), M, K, lda,
+            B.codes.data_ptr(), B.scales.data_ptr(), N, ldb, bp, bdt, act, rp, ldr, cp, cdt, ldc, qc,
+            ldq, qs, wp, wn)
+    return out
+
+
+# ---------------------------------------------------------------- experts
+@dataclasses.dataclass(slots=True)
+class Fp8Experts:
+    """One block-scaled weight matrix for each expert: value = code·scale."""
+    codes: "object"      # [E, N, K] float8_e4m3fn, unit column stride
+    scales: "object"     # [E, ceil(N/128), ceil(K/128)] float32
+
+    def expert(self, e: int) -> Fp8Matrix:
+        """The weights of expert e, as fp8_gemm takes them (a view)."""
+        return Fp8Matrix(self.codes[e], self.scales[e], FP8_BLOCK)
+
+
+@dataclasses.dataclass(slots=True)
+class Routing:
+    """Which experts each token takes, and the slots token·top_k + j by expert."""
+    ids: "object"        # [T, top_k] int32; -1: none
+    weights: "object"    # [T, top_k] float32
+    offsets: "object"    # [E + 1] int32: expert e's positions in order
+    order: "object"      # [T·top_k] int32: slots sorted by expert, -1 behind the last
+
+
+_SCORES = {"softmax": _native.SCORE_SOFTMAX, "sigmoid": _native.SCORE_SIGMOID}
+
+
+def expert_workspace_bytes(which: int, T: int, top_k: int, n_experts: int, N: int = 0, K: int = 0) -> int:
+    return int(_native.lib().gptq_expert_workspace_bytes(which, T, top_k, n_experts, N, K))
+
+
+def _expert_workspace(which, T, k, E, N, K, ws, dev):
+    """(address, bytes, tensor to keep) of an experts' call's workspace."""
+    if ws is None:
+        need = _native.lib().gptq_expert_workspace_bytes(which, T, k, E, N, K)
+        if need <= 256:
+            return None, 0, None
+        ws = _workspace(need, dev)
+    else:
+        _ws_check(ws, dev)
+    return ws.data_ptr(), ws.numel(), ws
+
+
+def moe_route(logits, top_k: int, scores: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+              group_top: int = 1, renormalize: bool = True, scale: float = 1.0, mask=None,
+              ws=None) -> Routing:
+    """Each token's top_k experts of logits [T, E] (float32/bfloat16/float16).
+
+    p = softmax or sigmoid of the logits; the choice goes by c = p + bias
+    (bias [E] float32; without one by the logits), among the top_groups of
+    `groups` groups of neighbouring experts with the largest sum of their
+    group_top (1 or 2) best c; ties to the lowest index.  weights = p of the
+    chosen, over their sum with renormalize, times scale.  A logit of -inf
+    excludes its expert; mask [T] bool: False for tokens that take none
+    (padding).  Slots without an expert have id -1 and weight 0.
+    ws: the workspace (allocated here when None; pass one to reuse)."""
+    empty, _, f32 = _t8()[:3]
+    i32 = _torch().int32
+    dt = _fp8_dtype(logits, "logits")
+    ld = _fp8_rows(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    sc = _SCORES.get(scores)
+    if sc is None:
+        raise ValueError(f"scores must be one of {sorted(_SCORES)} (got {scores!r})")
+    bp, mp = None, None
+    if bias is not None:
+        if bias.dtype != f32 or bias.shape != (E,) or not bias.is_contiguous() or bias.device != dev:
+            raise ValueError(f"bias must be contiguous float32 of shape {(E,)} on {dev}")
+        bp = bias.data_ptr()
+    if mask is not None:
+        if mask.dtype != _torch().bool or mask.shape != (T,) or not mask.is_contiguous() or mask.device != dev:
+            raise ValueError(f"mask must be contiguous bool of shape {(T,)} on {dev}")
+        mp = mask.data_ptr()
+    wp, wn, ws = _expert_workspace(_native.WS_MOE, T, top_k, E, 0, 0, ws, dev)
+    k = max(int(top_k), 0)   # a bad top_k is the library's to refuse
+    r = Routing(empty((T, k), dtype=i32, device=dev), empty((T, k), dtype=f32, device=dev),
+                empty(E + 1, dtype=i32, device=dev), empty(T * k, dtype=i32, device=dev))
+    _launch(dev, _native.lib().gptq_moe_route, logits.data_ptr(), dt, T, E, ld, bp, mp, sc, top_k,
+            groups, top_groups, group_top, 1 if renormalize else 0, scale, r.ids.data_ptr(),
+            r.weights.data_ptr(), r.offsets.data_ptr(), r.order.data_ptr(), wp, wn)
+    return r
+
+
+def moe_plan(ids, weights, n_experts: int, ws=None) -> Routing:
+    """A Routing of experts that were chosen elsewhere: ids [T, top_k] int32
+    (below 0 or from n_experts on: none), weights [T, top_k] float32."""
+    empty, _, f32 = _t8()[:3]
+    i32 = _torch().int32
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, top_k]")
+    T, k = ids.shape
+    dev = ids.device
+    _require(ids, "ids", i32, (T, k))
+    _require(weights, "weights", f32, (T, k), dev)
+    wp, wn, ws = _expert_workspace(_native.WS_MOE, T, k, n_experts, 0, 0, ws, dev)
+    r = Routing(ids, weights, empty(max(n_experts, 0) + 1, dtype=i32, device=dev),
+                empty(T * k, dtype=i32, device=dev))
+    _launch(dev, _native.lib().gptq_moe_plan, ids.data_ptr(), T, k, n_experts, r.offsets.data_ptr(),
+            r.order.data_ptr(), wp, wn)
+    return r
+
+
+def fp8_quantize_experts(W, out: Fp8Experts | None = None) -> Fp8Experts:
+    """W [E, N, K] (float32/bfloat16/float16) in e4m3, each expert's matrix as
+    fp8_quantize(W[e], 128) gives it."""
+    if W.dim() != 3:
+        raise ValueError("W must be [E, N, K]")
+    empty, e4m3, f32 = _t8()[:3]
+    E, N, K = W.shape
+    if out is None:
+        ld = (K + 15) // 16 * 16
+        out = Fp8Experts(empty((E, N, ld), dtype=e4m3, device=W.device)[:, :, :K],
+                         empty((E, (N + FP8_BLOCK - 1) // FP8_BLOCK, (K + FP8_BLOCK - 1) // FP8_BLOCK),
+                               dtype=f32, device=W.device))
+    elif out.codes.shape != W.shape or out.codes.device != W.device:
+        raise ValueError(f"out must have shape {tuple(W.shape)} on {W.device}")
+    _experts_arg(out, "out", W.device)
+    for e in range(E):
+        fp8_quantize(W[e], FP8_BLOCK, out=out.expert(e))
+    return out
+
+
+def _experts_arg(m: Fp8Experts, name, device):
+    """(E, N, K, row stride, expert stride) of the experts' weights after their checks."""
+    c, s = m.codes, m.scales
+    _, e4m3, f32, _, _, _ = _t8()
+    if c.dtype != e4m3:
+        raise ValueError(f"{name}.codes must be float8_e4m3fn (got {c.dtype})")
+    if c.dim() != 3:
+        raise ValueError(f"{name}.codes must be [E, N, K]")
+    E, N, K = c.shape
+    next_, ld, one = c.stride()
+    if N <= 1:
+        ld = K
+    if E <= 1:
+        next_ = 0
+    if (one != 1 and K > 1) or ld < K or next_ < 0:
+        raise ValueError(f"{name}.codes must have unit column stride")
+    want = (E, (N + FP8_BLOCK - 1) // FP8_BLOCK, (K + FP8_BLOCK - 1) // FP8_BLOCK)
+    if s.dtype != f32 or s.shape != want or not s.is_contiguous():
+        raise ValueError(f"{name}.scales must be contiguous float32 of shape {want} "
+                         f"(got {s.dtype}, {tuple(s.shape)})")
+    if c.device != device or s.device != device:
+        raise ValueError(f"{name} is on {c.device} (scales on {s.device}), expected {device}")
+    return E, N, K, ld, next_
+
+
+def _routing_arg(r: Routing, E, device):
+    """(T, top_k) of a routing over E experts after its checks."""
+    _, _, f32, _, _, _ = _t8()
+    i32 = _torch().int32
+    if r.ids.dim() != 2:
+        raise ValueError("routing.ids must be [T, top_k]")
+    T, k = r.ids.shape
+    for t, name, dtype, shape in ((r.ids, "ids", i32, (T, k)), (r.weights, "weights", f32, (T, k)),
+                                  (r.offsets, "offsets", i32, (E + 1,)), (r.order, "order", i32, (T * k,))):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"routing.{name} must be contiguous {dtype} of shape {shape} on {device} "
+                             f"(got {t.dtype}, {tuple(t.shape)} on {t.device})")
+    return T, k
+
+
+def fp8_expert_gated_gemm(A: Fp8Matrix, routing: Routing, gate: Fp8Experts, up: Fp8Experts,
+                          activation: str = "silu", out_dtype=None, out=None, ws=None):
+    """act(x·gate_eᵀ)·(x·up_eᵀ) of each token x of A [T, K] and each of its
+    experts e, rows in the order of routing.order: an Fp8Matrix [T·top_k, N]
+    with block_rows 1, or a tensor of out_dtype where that is given; `out` is
+    either, to be filled.  Rows behind the last that has an expert are left as
+    they were.  ws: as for fp8_gated_gemm."""
+    T, K, lda, dev = _fp8_arg(A, "A", 1)
+    E, N, kg, ldg, next_g = _experts_arg(gate, "gate", dev)
+    eu, nu, ku, ldu, next_u = _experts_arg(up, "up", dev)
+    if kg != K or ku != K or nu != N or eu != E:
+        raise ValueError(f"A has {K} columns; gate {(E, N, kg)} and up {(eu, nu, ku)} do not fit")
+    tr, k = _routing_arg(routing, E, dev)
+    if tr != T:
+        raise ValueError(f"A has {T} rows, the routing {tr} tokens")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)} (got {activation!r})")
+    M = T * k
+    cp, cdt, ldc, qc, ldq, qs = None, 0, 0, None, 0, None
+    if out is None and out_dtype is None:
+        out, ldq = _fp8_new(M, N, 1, dev)
+        qc, qs = out.codes.data_ptr(), out.scales.data_ptr()
+    elif isinstance(out, Fp8Matrix):
+        if out_dtype is not None:
+            raise ValueError("an Fp8Matrix out has no out_dtype")
+        mo, no, ldq, _ = _fp8_arg(out, "out", 1, dev)
+        if (mo, no) != (M, N):
+            raise ValueError(f"out must have shape {(M, N)} (got {(mo, no)})")
+        qc, qs = out.codes.data_ptr(), out.scales.data_ptr()
+    else:
+        if out is None:
+            out = _t8()[0]((M, N), dtype=out_dtype, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out must be {out_dtype} (got {out.dtype})")
+        cdt = _fp8_dtype(out, "out")
+        ldc = _fp8_out(out, "out", out.dtype, (M, N), dev)
+        cp = out.data_ptr()
+    wp, wn, ws = _expert_workspace(_native.WS_EXPERT_GATED, T, k, E, N, K, ws, dev)
+    _launch(dev, _native.lib().gptq_fp8_expert_gated_gemm, A.codes.data_ptr(), A.scales.data_ptr(), T,
+            K, lda, k, routing.offsets.data_ptr(), routing.order.data_ptr(), E, gate.codes.data_ptr(),
+            gate.scales.data_ptr(), ldg, next_g, up.codes.data_ptr(), up.scales.data_ptr(), ldu, next_u,
+            N, act, cp, cdt, ldc, qc, ldq, qs, wp, wn)
+    return out
+
+
+def fp8_expert_gemm(H: Fp8Matrix, routing: Routing, down: Fp8Experts, residual=None, out_dtype=None,
+                    out=None, ws=None):
+    """Σ_j weights[t, j]·(h·down_eᵀ) + residual[t]: H [T·top_k, K] in the order
+    of routing.order, as fp8_expert_gated_gemm gives it; the result [T, N] in
+    out_dtype (bfloat16 unless given, or `out`'s type), rounded once.
+    residual [T, N] of that type; out may be residual itself.
+    ws: the workspace (allocated here when None; pass one to reuse)."""
+    M, K, ldh, dev = _fp8_arg(H, "H", 1)
+    E, N, kd, ldd, next_d = _experts_arg(down, "down", dev)
+    if kd != K:
+        raise ValueError(f"H has {K} columns, down has {kd}")
+    T, k = _routing_arg(routing, E, dev)
+    if T * k != M:
+        raise ValueError(f"H has {M} rows, the routing {T} tokens of {k} slots")
+    if out is None:
+        out = _t8()[0]((T, N), dtype=out_dtype or _torch().bfloat16, device=dev)
+        ldc = N
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out must be {out_dtype} (got {out.dtype})")
+        ldc = _fp8_out(out, "out", out.dtype, (T, N), dev)
+    cdt = _fp8_dtype(out, "out")
+    rp, ldr = None, 0
+    if residual is not None:
+        ldr = _fp8_out(residual, "residual", out.dtype, (T, N), dev)
+        rp = residual.data_ptr()
+    wp, wn, ws = _expert_workspace(_native.WS_EXPERT_GEMM, T, k, E, N, K, ws, dev)
+    _launch(dev, _native.lib().gptq_fp8_expert_gemm, H.codes.data_ptr(), H.scales.data_ptr(), T, K, ldh,
+            k, routing.ids.data_ptr(), routing.weights.data_ptr(), routing.offsets.data_ptr(),
+            routing.order.data_ptr(), E, down.codes.data_ptr(), down.scales.data_ptr(), ldd, next_d, N,
+            rp, ldr, out.data_ptr(), cdt, ldc, wp, wn)
     return out
 
 

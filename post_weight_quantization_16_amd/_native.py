@@ -16,9 +16,12 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_NOT_SPD, ERR_WORKSPACE, ERR_HIP, ERR_I
 F32, BF16, F16 = 0, 1, 2
 # workspace kinds
 WS_HESSIAN, WS_PREPARE, WS_QUANTIZE, WS_OBQ, WS_W4A16, WS_LAYER = 0, 1, 2, 3, 4, 5
-WS_FP8_GEMM, WS_FP8_GATED = 6, 7
+WS_FP8_GEMM, WS_FP8_GATED, WS_FP8_LINEAR = 6, 7, 8
+WS_MOE, WS_EXPERT_GATED, WS_EXPERT_GEMM = 9, 10, 11   # expert_workspace_bytes
 # gptq_activation
 ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2
+# gptq_scores
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 EXPORTS = (
     "gptq_workspace_bytes",
@@ -38,6 +41,12 @@ EXPORTS = (
     "gptq_rmsnorm_fp8",
     "gptq_fp8_gemm",
     "gptq_fp8_gated_gemm",
+    "gptq_fp8_linear",
+    "gptq_expert_workspace_bytes",
+    "gptq_moe_route",
+    "gptq_moe_plan",
+    "gptq_fp8_expert_gated_gemm",
+    "gptq_fp8_expert_gemm",
     "gptq_timing",
     "gptq_timing_read",
     "gptq_last_error",
@@ -164,6 +173,24 @@ def lib() -> ctypes.CDLL:
     L.gptq_fp8_gated_gemm.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
                                       _i64, _int, _vp, _int, _i64, _vp, _i64, _vp, _vp, _sz, _vp]
     L.gptq_fp8_gated_gemm.restype = _int
+    L.gptq_fp8_linear.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _int, _int,
+                                  _vp, _i64, _vp, _int, _i64, _vp, _i64, _vp, _vp, _sz, _vp]
+    L.gptq_fp8_linear.restype = _int
+    L.gptq_expert_workspace_bytes.argtypes = [_int, _i64, _i64, _i64, _i64, _i64]
+    L.gptq_expert_workspace_bytes.restype = _sz
+    L.gptq_moe_route.argtypes = [_vp, _int, _i64, _i64, _i64, _vp, _vp, _int, _int, _int, _int, _int,
+                                 _int, ctypes.c_double, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+    L.gptq_moe_route.restype = _int
+    L.gptq_moe_plan.argtypes = [_vp, _i64, _int, _i64, _vp, _vp, _vp, _sz, _vp]
+    L.gptq_moe_plan.restype = _int
+    L.gptq_fp8_expert_gated_gemm.argtypes = [_vp, _vp, _i64, _i64, _i64, _int, _vp, _vp, _i64, _vp,
+                                             _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _int, _vp,
+                                             _int, _i64, _vp, _i64, _vp, _vp, _sz, _vp]
+    L.gptq_fp8_expert_gated_gemm.restype = _int
+    L.gptq_fp8_expert_gemm.argtypes = [_vp, _vp, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _i64,
+                                       _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _int, _i64, _vp,
+                                       _sz, _vp]
+    L.gptq_fp8_expert_gemm.restype = _int
     L.gptq_timing.argtypes = [_int]
     L.gptq_timing.restype = _int
     L.gptq_timing_read.argtypes = [ctypes.POINTER(ctypes.c_float), _int]

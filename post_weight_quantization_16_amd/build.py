@@ -33,6 +33,9 @@ SOURCES = [
     ("w4a16.hip", "w4a16.o", []),
     ("fp8_quant.hip", "fp8_quant.o", []),
     ("fp8_gemm.hip", "fp8_gemm.o", []),
+    ("fp8_linear.hip", "fp8_linear.o", []),
+    ("fp8_expert.hip", "fp8_expert.o", []),
+    ("moe.hip", "moe.o", []),
 ] + [("sweep.hip", f"sweep_g{g}.o", [f"-DGQ_SWEEP_G={g}"]) for g in (0, 32, 64, 128)]
 
 FLAGS = [

@@ -133,6 +133,20 @@ int check_fp8_size(int64_t rows, int64_t cols) {
     return fail(GPTQ_ERR_INVALID_ARG, "rows * cols must be at most 2^34 (got %lld)", (long long)(rows * cols));
   return GPTQ_OK;
 }
+// Tokens, slots and experts of the experts' calls.
+int check_slots(int64_t T, int64_t k, int64_t E) {
+  if (E < 1 || E > gq::kMaxExperts)
+    return fail(GPTQ_ERR_INVALID_ARG, "n_experts must be in [1, %d]", gq::kMaxExperts);
+  if (k < 1 || k > E || k > gq::kMaxTopK)
+    return fail(GPTQ_ERR_INVALID_ARG, "top_k must be in [1, min(n_experts, %d)]", gq::kMaxTopK);
+  if (T < 0 || T > kMaxDout || T * k > (int64_t(1) << 30))
+    return fail(GPTQ_ERR_INVALID_ARG, "T must be in [0, %lld] and T * top_k at most 2^30", (long long)kMaxDout);
+  return GPTQ_OK;
+}
+int check_moe_ws(void* ws, size_t ws_bytes, int64_t T, int64_t E, int64_t k, const char* what) {
+  const size_t need = gq::moe_ws_bytes(T, E, k);
+  return ws || need > 256 ? check_ws(ws, ws_bytes, need, what) : GPTQ_OK;
+}
 // Element pointers must be aligned to their type (the calls that take any
 // byte address say so).
 bool misaligned(const void* p, int dt) { return (uintptr_t)p % (dt == GPTQ_F32 ? 4 : 2) != 0; }
@@ -237,10 +251,12 @@ size_t gptq_workspace_bytes(int which, int64_t d_out, int64_t d_in, int64_t n_to
       return gq::w4a16_ws_bytes(n_tok, d_out, d_in);
     case GPTQ_WS_FP8_GEMM:
     case GPTQ_WS_FP8_GATED:
+    case GPTQ_WS_FP8_LINEAR:
       if (d_out <= 0 || d_out > kMaxDout || n_tok < 0 || n_tok > kMaxDout) return 0;
       if (n_tok == 0) return 256;
-      return which == GPTQ_WS_FP8_GEMM ? gq::fp8_gemm_ws_bytes(n_tok, d_out, d_in)
-                                       : gq::fp8_gated_ws_bytes(n_tok, d_out, d_in);
+      return which == GPTQ_WS_FP8_GEMM    ? gq::fp8_gemm_ws_bytes(n_tok, d_out, d_in)
+             : which == GPTQ_WS_FP8_GATED ? gq::fp8_gated_ws_bytes(n_tok, d_out, d_in)
+                                          : gq::fp8_linear_ws_bytes(n_tok, d_out, d_in);
     default:
       return 0;
   }
@@ -638,6 +654,170 @@ int gptq_fp8_gated_gemm(const uint8_t* A, const float* a_scales, int64_t M, int6
                                       activation, C, c_dtype, ldc, codes, ld_codes, scales, ws,
                                       (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail("fp8_gated_gemm", e);
+  return GPTQ_OK;
+}
+
+int gptq_fp8_linear(const uint8_t* A, const float* a_scales, int64_t M, int64_t K, int64_t lda,
+                    const uint8_t* B, const float* b_scales, int64_t N, int64_t ldb,
+                    const void* bias, int bias_dtype, int activation, const void* R, int64_t ld_r,
+                    void* C, int c_dtype, int64_t ldc, uint8_t* codes, int64_t ld_codes,
+                    float* scales, void* ws, size_t ws_bytes, gptq_stream stream) {
+  int rc = check_fp8_shape(M, K, "M", "K");
+  if (rc) return rc;
+  if (N <= 0 || N > kMaxDout)
+    return fail(GPTQ_ERR_INVALID_ARG, "N must be in [1, %lld]", (long long)kMaxDout);
+  if (activation < -1 || activation > GPTQ_ACT_GELU_TANH)
+    return fail(GPTQ_ERR_INVALID_ARG, "unknown activation %d", activation);
+  if (bias && !valid_dtype(bias_dtype))
+    return fail(GPTQ_ERR_INVALID_ARG, "unknown bias_dtype %d", bias_dtype);
+  if (C && !valid_dtype(c_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown c_dtype %d", c_dtype);
+  if (lda < K || ldb < K || (R && ld_r < N) || (C && ldc < N) || (codes && ld_codes < N))
+    return fail(GPTQ_ERR_INVALID_ARG, "a row stride is smaller than its row");
+  if (M == 0) return GPTQ_OK;
+  if (!A || !a_scales || !B || !b_scales)
+    return fail(GPTQ_ERR_INVALID_ARG, "A, B and their scales must not be NULL");
+  if (!codes != !scales) return fail(GPTQ_ERR_INVALID_ARG, "codes and scales go together");
+  if (!C == !codes) return fail(GPTQ_ERR_INVALID_ARG, "give C or codes, one of the two");
+  if (R && !C) return fail(GPTQ_ERR_INVALID_ARG, "a residual goes with C, not with codes");
+  if (R && R == C && ld_r != ldc)
+    return fail(GPTQ_ERR_INVALID_ARG, "C in the place of the residual needs its row stride");
+  if (misaligned(a_scales, GPTQ_F32) || misaligned(b_scales, GPTQ_F32) ||
+      misaligned(scales, GPTQ_F32) || misaligned(bias, bias_dtype) || misaligned(R, c_dtype) ||
+      misaligned(C, c_dtype))
+    return fail(GPTQ_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+  if (ws && (rc = check_ws(ws, ws_bytes, gq::fp8_linear_ws_bytes(M, N, K), "fp8_linear"))) return rc;
+  hipError_t e = gq::fp8_linear_launch(A, a_scales, M, K, lda, B, b_scales, N, ldb, bias, bias_dtype,
+                                       activation, R, ld_r, C, c_dtype, ldc, codes, ld_codes, scales,
+                                       ws, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail("fp8_linear", e);
+  return GPTQ_OK;
+}
+
+size_t gptq_expert_workspace_bytes(int which, int64_t T, int64_t top_k, int64_t n_experts, int64_t N,
+                                   int64_t K) {
+  if (check_slots(T, top_k, n_experts)) return 0;
+  if (which == GPTQ_WS_MOE) return gq::moe_ws_bytes(T, n_experts, top_k);
+  if (which != GPTQ_WS_EXPERT_GATED && which != GPTQ_WS_EXPERT_GEMM) return 0;
+  if (N <= 0 || N > kMaxDout || K <= 0 || K > kMaxDin) return 0;
+  if (T == 0) return 256;
+  return which == GPTQ_WS_EXPERT_GATED ? gq::fp8_expert_gated_ws_bytes(T, top_k, n_experts, N, K)
+                                       : gq::fp8_expert_gemm_ws_bytes(T, top_k, n_experts, N, K);
+}
+
+int gptq_moe_route(const void* logits, int dtype, int64_t T, int64_t n_experts, int64_t ld,
+                   const float* bias, const uint8_t* mask, int scores, int top_k, int n_groups,
+                   int top_groups, int group_top, int renormalize, double scale, int32_t* ids,
+                   float* weights, int32_t* offsets, int32_t* order, void* ws, size_t ws_bytes,
+                   gptq_stream stream) {
+  int rc = check_slots(T, top_k, n_experts);
+  if (rc) return rc;
+  if (!valid_dtype(dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (ld < n_experts) return fail(GPTQ_ERR_INVALID_ARG, "ld < n_experts");
+  if (scores != GPTQ_SCORE_SOFTMAX && scores != GPTQ_SCORE_SIGMOID)
+    return fail(GPTQ_ERR_INVALID_ARG, "unknown scores %d", scores);
+  if (n_groups < 1 || n_groups > gq::kMaxGroups || n_experts % n_groups)
+    return fail(GPTQ_ERR_INVALID_ARG, "n_groups must be in [1, %d] and divide n_experts", gq::kMaxGroups);
+  if (top_groups < 1 || top_groups > n_groups || top_k > top_groups * (n_experts / n_groups))
+    return fail(GPTQ_ERR_INVALID_ARG, "top_groups must be in [1, n_groups] and hold top_k experts");
+  if (group_top != 1 && group_top != 2)
+    return fail(GPTQ_ERR_INVALID_ARG, "group_top must be 1 or 2 (got %d)", group_top);
+  if (renormalize != 0 && renormalize != 1)
+    return fail(GPTQ_ERR_INVALID_ARG, "renormalize must be 0 or 1");
+  if (!std::isfinite(scale)) return fail(GPTQ_ERR_INVALID_ARG, "scale must be finite");
+  if (T > 0 && !offsets != !order) return fail(GPTQ_ERR_INVALID_ARG, "offsets and order go together");
+  if (T == 0 && !offsets) return GPTQ_OK;
+  if (T > 0 && (!logits || !ids || !weights))
+    return fail(GPTQ_ERR_INVALID_ARG, "logits, ids and weights must not be NULL");
+  if (misaligned(logits, dtype) || misaligned(bias, GPTQ_F32) || misaligned(ids, GPTQ_F32) ||
+      misaligned(weights, GPTQ_F32) || misaligned(offsets, GPTQ_F32) || misaligned(order, GPTQ_F32))
+    return fail(GPTQ_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+  if (offsets && (rc = check_moe_ws(ws, ws_bytes, T, n_experts, top_k, "moe_route"))) return rc;
+  hipError_t e = gq::moe_route_launch(logits, dtype, T, (int)n_experts, ld, bias, mask, scores, top_k,
+                                      n_groups, top_groups, group_top, renormalize, scale, ids,
+                                      weights, offsets, order, ws, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail("moe_route", e);
+  return GPTQ_OK;
+}
+
+int gptq_moe_plan(const int32_t* ids, int64_t T, int top_k, int64_t n_experts, int32_t* offsets,
+                  int32_t* order, void* ws, size_t ws_bytes, gptq_stream stream) {
+  int rc = check_slots(T, top_k, n_experts);
+  if (rc) return rc;
+  if (!offsets || (T > 0 && (!ids || !order)))
+    return fail(GPTQ_ERR_INVALID_ARG, "ids, offsets and order must not be NULL");
+  if (misaligned(ids, GPTQ_F32) || misaligned(offsets, GPTQ_F32) || misaligned(order, GPTQ_F32))
+    return fail(GPTQ_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+  if ((rc = check_moe_ws(ws, ws_bytes, T, n_experts, top_k, "moe_plan"))) return rc;
+  hipError_t e = gq::moe_plan_launch(ids, T, top_k, (int)n_experts, offsets, order, ws, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail("moe_plan", e);
+  return GPTQ_OK;
+}
+
+int gptq_fp8_expert_gated_gemm(const uint8_t* A, const float* a_scales, int64_t T, int64_t K,
+                               int64_t lda, int top_k, const int32_t* offsets, const int32_t* order,
+                               int64_t n_experts, const uint8_t* G, const float* g_scales,
+                               int64_t ldg, int64_t next_g, const uint8_t* U, const float* u_scales,
+                               int64_t ldu, int64_t next_u, int64_t N, int activation, void* C,
+                               int c_dtype, int64_t ldc, uint8_t* codes, int64_t ld_codes,
+                               float* scales, void* ws, size_t ws_bytes, gptq_stream stream) {
+  int rc = check_slots(T, top_k, n_experts);
+  if (rc || (rc = check_fp8_shape(T, K, "T", "K"))) return rc;
+  if (N <= 0 || N > kMaxDout)
+    return fail(GPTQ_ERR_INVALID_ARG, "N must be in [1, %lld]", (long long)kMaxDout);
+  if (activation < GPTQ_ACT_SILU || activation > GPTQ_ACT_GELU_TANH)
+    return fail(GPTQ_ERR_INVALID_ARG, "unknown activation %d", activation);
+  if (C && !valid_dtype(c_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown c_dtype %d", c_dtype);
+  if (lda < K || ldg < K || ldu < K || (C && ldc < N) || (codes && ld_codes < N))
+    return fail(GPTQ_ERR_INVALID_ARG, "a row stride is smaller than its row");
+  if (next_g < 0 || next_u < 0) return fail(GPTQ_ERR_INVALID_ARG, "next_g and next_u must be >= 0");
+  if (T == 0) return GPTQ_OK;
+  if (!A || !a_scales || !G || !g_scales || !U || !u_scales || !offsets || !order)
+    return fail(GPTQ_ERR_INVALID_ARG, "A, G, U, their scales, offsets and order must not be NULL");
+  if (!codes != !scales) return fail(GPTQ_ERR_INVALID_ARG, "codes and scales go together");
+  if (!C == !codes) return fail(GPTQ_ERR_INVALID_ARG, "give C or codes, one of the two");
+  if (misaligned(a_scales, GPTQ_F32) || misaligned(g_scales, GPTQ_F32) ||
+      misaligned(u_scales, GPTQ_F32) || misaligned(scales, GPTQ_F32) || misaligned(C, c_dtype) ||
+      misaligned(offsets, GPTQ_F32) || misaligned(order, GPTQ_F32))
+    return fail(GPTQ_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+  const size_t need = gq::fp8_expert_gated_ws_bytes(T, top_k, n_experts, N, K);
+  if (ws && (rc = check_ws(ws, ws_bytes, need, "fp8_expert_gated_gemm"))) return rc;
+  hipError_t e = gq::fp8_expert_gated_launch(A, a_scales, T, K, lda, top_k, offsets, order,
+                                             (int)n_experts, G, g_scales, ldg, next_g, U, u_scales,
+                                             ldu, next_u, N, activation, C, c_dtype, ldc, codes,
+                                             ld_codes, scales, ws, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail("fp8_expert_gated_gemm", e);
+  return GPTQ_OK;
+}
+
+int gptq_fp8_expert_gemm(const uint8_t* H, const float* h_scales, int64_t T, int64_t K, int64_t ldh,
+                         int top_k, const int32_t* ids, const float* weights, const int32_t* offsets,
+                         const int32_t* order, int64_t n_experts, const uint8_t* D,
+                         const float* d_scales, int64_t ldd, int64_t next_d, int64_t N,
+                         const void* R, int64_t ld_r, void* C, int c_dtype, int64_t ldc, void* ws,
+                         size_t ws_bytes, gptq_stream stream) {
+  int rc = check_slots(T, top_k, n_experts);
+  if (rc || (rc = check_fp8_shape(T, K, "T", "K"))) return rc;
+  if (N <= 0 || N > kMaxDout)
+    return fail(GPTQ_ERR_INVALID_ARG, "N must be in [1, %lld]", (long long)kMaxDout);
+  if (!valid_dtype(c_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown c_dtype %d", c_dtype);
+  if (ldh < K || ldd < K || ldc < N || (R && ld_r < N))
+    return fail(GPTQ_ERR_INVALID_ARG, "a row stride is smaller than its row");
+  if (next_d < 0) return fail(GPTQ_ERR_INVALID_ARG, "next_d must be >= 0");
+  if (T == 0) return GPTQ_OK;
+  if (!H || !h_scales || !D || !d_scales || !ids || !weights || !offsets || !order || !C)
+    return fail(GPTQ_ERR_INVALID_ARG, "H, D, their scales, ids, weights, offsets, order and C must not be NULL");
+  if (R && R == C && ld_r != ldc)
+    return fail(GPTQ_ERR_INVALID_ARG, "C in the place of the residual needs its row stride");
+  if (misaligned(h_scales, GPTQ_F32) || misaligned(d_scales, GPTQ_F32) || misaligned(ids, GPTQ_F32) ||
+      misaligned(weights, GPTQ_F32) || misaligned(offsets, GPTQ_F32) || misaligned(order, GPTQ_F32) ||
+      misaligned(R, c_dtype) || misaligned(C, c_dtype))
+    return fail(GPTQ_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+  const size_t need = gq::fp8_expert_gemm_ws_bytes(T, top_k, n_experts, N, K);
+  if ((ws || need > 256) && (rc = check_ws(ws, ws_bytes, need, "fp8_expert_gemm"))) return rc;
+  hipError_t e = gq::fp8_expert_gemm_launch(H, h_scales, T, K, ldh, top_k, ids, weights, offsets, order,
+                                            (int)n_experts, D, d_scales, ldd, next_d, N, R, ld_r, C,
+                                            c_dtype, ldc, ws, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail("fp8_expert_gemm", e);
   return GPTQ_OK;
 }
 

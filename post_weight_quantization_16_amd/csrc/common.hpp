@@ -202,6 +202,38 @@ hipError_t fp8_gated_launch(const uint8_t* A, const float* sa, int64_t M, int64_
                             int64_t ldc, uint8_t* codes, int64_t ld_codes, float* sc, void* ws,
                             hipStream_t s);
 
+size_t fp8_linear_ws_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t fp8_linear_launch(const uint8_t* A, const float* sa, int64_t M, int64_t K, int64_t lda,
+                             const uint8_t* B, const float* sb, int64_t N, int64_t ldb,
+                             const void* bias, int bias_dt, int act, const void* R, int64_t ldr,
+                             void* C, int c_dt, int64_t ldc, uint8_t* codes, int64_t ld_codes,
+                             float* sc, void* ws, hipStream_t s);
+
+// ---------------------------------------------------------------- experts
+constexpr int kMaxExperts = 1024, kMaxTopK = 64, kMaxGroups = 16;
+size_t moe_ws_bytes(int64_t T, int64_t E, int64_t k);
+hipError_t moe_route_launch(const void* X, int dt, int64_t T, int E, int64_t ld, const float* bias,
+                            const uint8_t* mask, int scores, int k, int groups, int top_groups,
+                            int group_top, int renorm, double scale, int32_t* ids, float* weights,
+                            int32_t* offsets, int32_t* order, void* ws, hipStream_t s);
+hipError_t moe_plan_launch(const int32_t* ids, int64_t T, int k, int E, int32_t* offsets,
+                           int32_t* order, void* ws, hipStream_t s);
+size_t fp8_expert_gated_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
+size_t fp8_expert_gemm_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
+hipError_t fp8_expert_gated_launch(const uint8_t* A, const float* sa, int64_t T, int64_t K,
+                                   int64_t lda, int k, const int32_t* offsets, const int32_t* order,
+                                   int E, const uint8_t* G, const float* sg, int64_t ldg,
+                                   int64_t next_g, const uint8_t* U, const float* su, int64_t ldu,
+                                   int64_t next_u, int64_t N, int act, void* C, int c_dt,
+                                   int64_t ldc, uint8_t* codes, int64_t ld_codes, float* sc,
+                                   void* ws, hipStream_t s);
+hipError_t fp8_expert_gemm_launch(const uint8_t* A, const float* sa, int64_t T, int64_t K,
+                                  int64_t lda, int k, const int32_t* ids, const float* weights,
+                                  const int32_t* offsets, const int32_t* order, int E,
+                                  const uint8_t* B, const float* sb, int64_t ldb, int64_t next,
+                                  int64_t N, const void* R, int64_t ldr, void* C, int c_dt,
+                                  int64_t ldc, void* ws, hipStream_t s);
+
 // ---------------------------------------------------------------- export
 hipError_t export_launch(int bits, int64_t m, int64_t d, int64_t ng, const uint32_t* qweight,
                          const float* scales, const uint8_t* zeros, uint32_t* qdense,

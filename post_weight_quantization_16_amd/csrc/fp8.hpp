@@ -92,6 +92,12 @@ template <> struct Elem<GPTQ_F16> {
   static __device__ __forceinline__ _Float16 down(float x) { return (_Float16)x; }
 };
 
+// Element `at` of type dt, widened.
+__device__ __forceinline__ float get1(const void* p, int dt, int64_t at) {
+  if (dt == GPTQ_F32) return static_cast<const float*>(p)[at];
+  return dt == GPTQ_BF16 ? (float)static_cast<const __bf16*>(p)[at] : (float)static_cast<const _Float16*>(p)[at];
+}
+
 // Eight consecutive elements as stored, `n` of them present (the others are
 // zero).
 // Full pieces are copied whole at whatever alignment the caller's rows have:
