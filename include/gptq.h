@@ -608,7 +608,8 @@ int gptq_fp8_expert_gated_gemm(const uint8_t* A, const float* a_scales, int64_t 
  *   y[t] = Σ_j weights[t,j]·(h[i(t,j)]·D_eᵀ) + residual[t], one rounding,
  * i(t,j) the sorted position of slot t·top_k + j; slots without an expert add
  * nothing.  Products as in gptq_fp8_gemm (exact with fp32 sums for GPTQ_F32);
- * the sum over j is fp32, in the order of j.
+ * the sum over j is fp32.  For GPTQ_BF16 its terms h·D_eᵀ may be rounded to 11
+ * bits first, an eighth of what C's own rounding may lose.
  *  H, h_scales      [T·top_k x K] activations by sorted position, row stride
  *                   ldh; rows from offsets[E] on are not read.
  *  ids, weights     [T x top_k]; offsets and order as gptq_moe_plan makes them

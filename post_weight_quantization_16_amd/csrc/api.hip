@@ -700,8 +700,8 @@ size_t gptq_expert_workspace_bytes(int which, int64_t T, int64_t top_k, int64_t 
   if (which != GPTQ_WS_EXPERT_GATED && which != GPTQ_WS_EXPERT_GEMM) return 0;
   if (N <= 0 || N > kMaxDout || K <= 0 || K > kMaxDin) return 0;
   if (T == 0) return 256;
-  return which == GPTQ_WS_EXPERT_GATED ? gq::fp8_expert_gated_ws_bytes(T, top_k, n_experts, N, K)
-                                       : gq::fp8_expert_gemm_ws_bytes(T, top_k, n_experts, N, K);
+  return which == GPTQ_WS_EXPERT_GATED ? gq::fp8_expert_gated_ws_bytes()
+                                       : gq::fp8_expert_gemm_ws_bytes(T, top_k, N);
 }
 
 int gptq_moe_route(const void* logits, int dtype, int64_t T, int64_t n_experts, int64_t ld,
@@ -779,7 +779,7 @@ int gptq_fp8_expert_gated_gemm(const uint8_t* A, const float* a_scales, int64_t 
       misaligned(u_scales, GPTQ_F32) || misaligned(scales, GPTQ_F32) || misaligned(C, c_dtype) ||
       misaligned(offsets, GPTQ_F32) || misaligned(order, GPTQ_F32))
     return fail(GPTQ_ERR_INVALID_ARG, "a pointer is not aligned to its type");
-  const size_t need = gq::fp8_expert_gated_ws_bytes(T, top_k, n_experts, N, K);
+  const size_t need = gq::fp8_expert_gated_ws_bytes();
   if (ws && (rc = check_ws(ws, ws_bytes, need, "fp8_expert_gated_gemm"))) return rc;
   hipError_t e = gq::fp8_expert_gated_launch(A, a_scales, T, K, lda, top_k, offsets, order,
                                              (int)n_experts, G, g_scales, ldg, next_g, U, u_scales,
@@ -812,7 +812,7 @@ int gptq_fp8_expert_gemm(const uint8_t* H, const float* h_scales, int64_t T, int
       misaligned(weights, GPTQ_F32) || misaligned(offsets, GPTQ_F32) || misaligned(order, GPTQ_F32) ||
       misaligned(R, c_dtype) || misaligned(C, c_dtype))
     return fail(GPTQ_ERR_INVALID_ARG, "a pointer is not aligned to its type");
-  const size_t need = gq::fp8_expert_gemm_ws_bytes(T, top_k, n_experts, N, K);
+  const size_t need = gq::fp8_expert_gemm_ws_bytes(T, top_k, N);
   if ((ws || need > 256) && (rc = check_ws(ws, ws_bytes, need, "fp8_expert_gemm"))) return rc;
   hipError_t e = gq::fp8_expert_gemm_launch(H, h_scales, T, K, ldh, top_k, ids, weights, offsets, order,
                                             (int)n_experts, D, d_scales, ldd, next_d, N, R, ld_r, C,

@@ -64,6 +64,8 @@ enum { kPlain = 0, kGated = 1, kLinear = 2 };
 // one expert's tokens, gathered; or neighbouring ones that are sorted by expert,
 // their partial sums stored at their slots.
 enum { kDense = 0, kGather = 1, kSorted = 2 };
+// Elements of fp16 that hold n of them, the fp32 numbers behind them aligned.
+__host__ __device__ inline int64_t align_scaled(int64_t n) { return (n + 7) / 8 * 8; }
 
 // ---------------------------------------------------------------- a block's contraction
 // 128 bytes of a row, this lane's 32 of them.
@@ -227,13 +229,18 @@ template <int BM, int BN, int WM, int WN, int NS> struct Tile {
   static constexpr int WAVES = (BM / WM) * (BN / WN), NT = WAVES * 64;
   static constexpr int MI = WM / 16, NI = WN / 16;
   static constexpr int SEGS = (BM + BN) / 8;            // 1-KB copies per stage
-  static constexpr int PER = SEGS / WAVES;              // ... per wave
+  static constexpr int PER = (SEGS + WAVES - 1) / WAVES;   // ... per wave
   static constexpr int SB = (BM + BN) * 128;            // bytes per stage
   static constexpr int SCALES = NS * SB;                // two buffers of scales
   static constexpr int SCB = BM * 32 + 256;
   static constexpr int SMEM = SCALES + 2 * SCB;
   static constexpr int SCOPIES = BM / 8 + 1;            // copies of eight blocks' scales
-  static_assert(SEGS % WAVES == 0 && NS >= 2 && NS <= 4, "copy plan");
+  static_assert(NS >= 2 && NS <= 4, "copy plan");
+  // Copy i of wave w; where the waves do not share the copies out evenly, some
+  // make the last one again, with the same bytes.
+  static __device__ __forceinline__ int seg(int w, int i) {
+    return SEGS % WAVES ? min(w * PER + i, SEGS - 1) : w * PER + i;
+  }
   static_assert((NS - 2) * PER <= 63, "vmcnt range");
   // waves a SIMD gets from the workgroups that fit in a CU's LDS: the
   // registers must leave room for them
@@ -261,7 +268,20 @@ __device__ __forceinline__ void tile_of(uint32_t L, uint32_t total, uint32_t tm,
   bn = in / rows;
 }
 
-enum { kStore = 0, kPartial = 1, kCodes = 2 };
+// Results as they are, fp32 sums to be joined, codes; and sums for bf16 results
+// in fp16, each row of a block of columns times a power of two of its own.
+enum { kStore = 0, kPartial = 1, kCodes = 2, kScaled = 3 };
+
+// The power of two for kScaled, from s = Σ|sa·sb| over the row's blocks: codes
+// are 448 at most, so a sum is below s·128·448² < s·2^24.63 and, times 2^-(11 +
+// exponent of s), below 2^14.63: fp16 holds it.  Usual sums are 2^9 to 2^12
+// smaller, still 2^15 above the last normal number of fp16.
+__device__ __forceinline__ int scaled_exponent(float s) {
+  return min(max((int)((__builtin_bit_cast(uint32_t, s) >> 23) & 0xFF) - 127, -100), 100) + 11;
+}
+__device__ __forceinline__ float power_of_two(int e) {
+  return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
+}
 
 // ---------------------------------------------------------------- rows by expert
 // The sorted positions in stretches of up to BM rows of one expert, numbered
@@ -392,7 +412,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
   uint32_t voff[KEEP ? T::PER : 1];
   if constexpr (KEEP) {
 #pragma unroll
-    for (int i = 0; i < T::PER; ++i) voff[i] = (uint32_t)seg_offset(w * T::PER + i, lane);
+    for (int i = 0; i < T::PER; ++i) voff[i] = (uint32_t)seg_offset(T::seg(w, i), lane);
   }
   const unsigned sbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)S;
   const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;   // blocks from here on: through registers
@@ -418,7 +438,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
       if constexpr (!KEEP) asm volatile("" : "+v"(l));   // not hoisted
 #pragma unroll
       for (int i = i0; i < i1; ++i) {
-        const int seg = w * T::PER + i;
+        const int seg = T::seg(w, i);
         // ordered before the reads by the stage barriers
         lds_copy16(sbase + buf + (unsigned)seg * 1024u, seg_base(seg) + (int64_t)(kbeg + st) * 128,
                    KEEP ? voff[KEEP ? i : 0] : (uint32_t)seg_offset(seg, l));
@@ -432,13 +452,13 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
         i32x4 v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int seg = w * T::PER + g + u;
+          const int seg = T::seg(w, g + u);
           const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((seg & 1) << 6);
           v[u] = piece16(seg_base(seg) + seg_offset(seg, lane) - p16, (int64_t)(kbeg + st) * 128 + p16, a.K);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          *reinterpret_cast<i32x4*>(S + buf + (w * T::PER + g + u) * 1024 + lane * 16) = v[u];
+          *reinterpret_cast<i32x4*>(S + buf + T::seg(w, g + u) * 1024 + lane * 16) = v[u];
       }
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
@@ -468,10 +488,25 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
     return {*reinterpret_cast<const i32x4*>(b + off), *reinterpret_cast<const i32x4*>(b + (off ^ 64))};
   };
 
+  float ssum[EPI == kScaled ? MI : 1];   // Σ|sa·sb| of each A piece's row
+  if constexpr (EPI == kScaled) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) ssum[i] = 0.f;
+  }
+  // a wave none of whose rows exist only copies
+  const bool idle = ROWS != kDense && wm * WM >= mleft;
   if (nst > 0) {
     copy_scales(0);
     for (int s0 = 0; s0 < NS - 1 && s0 < nst; ++s0) copy(s0, 0, T::PER);
     stage_barrier<T::PER>(min(nst - 1, NS - 2));
+  }
+  if (nst > 0 && idle) {
+    for (int st = 0; st < nst; ++st) {
+      if (st + NS - 1 < nst) copy(st + NS - 1, 0, T::PER);
+      if ((st & 7) == 0 && st + 8 < nst) copy_scales((st >> 3) + 1);
+      stage_barrier<T::PER>(min(nst - 1, st + NS - 1) - (st + 1));
+    }
+  } else if (nst > 0) {
     // The loop is software-pipelined by hand: step (i, j) multiplies A piece i
     // by B piece j and adds the product of the step before, so the matrix
     // core works while the adds run; A pieces are read one ahead, and the
@@ -502,6 +537,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
         sa = sn;
 #pragma unroll
         for (int q = 0; q < NB; ++q) s[q] = sa * sb[q];
+        if constexpr (EPI == kScaled) ssum[i] += fabsf(s[0]);
         if (i + 1 < MI) {
           ra = read_a(b, i + 1);
           sn = *reinterpret_cast<const float*>(sc + soff + (i + 1) * 512);
@@ -556,8 +592,8 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
         for (int r = 0; r < 4; ++r)
           acc[NI - G + g][MI - 1][r] = __builtin_fmaf(p[g][r], sp[g], acc[NI - G + g][MI - 1][r]);
     }
-    __syncthreads();   // the epilogue reuses the stage buffers
   }
+  if (nst > 0) __syncthreads();   // the epilogue reuses the stage buffers
 
   const int nl = wn * WC + 4 * (lane >> 4);   // this lane's first column in the tile
   if constexpr (EPI == kPartial) {
@@ -592,6 +628,27 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
       for (int j = 0; j < NI; ++j) {
         const int half = GATED ? j / (NI / 2) : 0, c = nl + (GATED ? j % (NI / 2) : j) * 16;
         put4<GPTQ_F32>(P, ((int64_t)half * a.M + row) * a.N + n0 + c, nleft - c, acc[j][i]);
+      }
+    }
+    return;
+  }
+  if constexpr (EPI == kScaled) {
+    // P: fp16 [slots][N], behind it the powers of two [slots][nb]
+    _Float16* P = reinterpret_cast<_Float16*>(a.P);
+    float* F = reinterpret_cast<float*>(P + align_scaled((int64_t)a.slots * a.N));
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int ml = wm * WM + i * 16 + l15;
+      if (ml >= mleft || row_of[ml] < 0) continue;
+      const int64_t row = row_of[ml];
+      const int e = scaled_exponent(ssum[i]);
+      const float f = power_of_two(-e);
+      if (lane < 16 && (wn * WC) % 128 == 0 && nl < nleft) F[row * a.nb + (n0 + nl) / 128] = power_of_two(e);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][i][r] *= f;
+        put4<GPTQ_F16>(P, row * a.N + n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
       }
     }
     return;

@@ -384,7 +384,8 @@ def test_expert_gemm(T, E, k, N, K, how):
     H, D, I = _values(h), _each(d), ids.cpu().numpy()
     for j, c in enumerate(["bf16", "f16", "f32"]):
         res = _randn(T, N, seed=5, std=2.0).to(_t(c)).cuda() if (T + j) % 2 else None
-        ref, bound = moe.combined(H, I, np.nan_to_num(_np(w)), D, None if res is None else _np(res), grouped=c != "f32")
+        ref, bound = moe.combined(H, I, np.nan_to_num(_np(w)), D, None if res is None else _np(res), grouped=c != "f32",
+                                  half_terms=c == "bf16" and T > 16)      # up to 16 tokens: no terms leave the kernel
         y = gq().fp8_expert_gemm(h, r, d, res, out_dtype=_t(c))
         _check(y, ref, bound, c, f"EXPERT GEMM {T}x{E}x{k} {N}x{K} {c}")
         assert _same(gq().fp8_expert_gemm(h, r, d, res, out_dtype=_t(c)), y)
@@ -510,7 +511,7 @@ def test_block_of_experts(T):
     _check_codes(_values(shared), ref, bound(False), "shared expert")
     ref, bound = moe.linear(_values(shared), _values(W[7]), None, None, _np(n.h))
     _check(s, ref, bound(True), "bf16", "shared expert back")
-    ref, bound = moe.combined((hv[:R], hs[:R]), I, _np(route.weights), _each(W[5]), _np(s), grouped=True)
+    ref, bound = moe.combined((hv[:R], hs[:R]), I, _np(route.weights), _each(W[5]), _np(s), grouped=True, half_terms=T > 16)
     _check(y, ref, bound, "bf16", f"BLOCK {T}")
 
 
