@@ -533,12 +533,14 @@ int gptq_fp8_linear(const uint8_t* A, const float* a_scales, int64_t M, int64_t 
  *           expert; -1 from position offsets[E] on.
  * The same expert may stand twice in a token's slots.  Tables that are not of
  * this form give undefined outputs, but no access outside the operands.
- * E <= 1024, top_k <= min(E, 64), T <= 2^24, T·top_k <= 2^30.  T == 0 is a
- * no-op but for offsets, which become zeros. */
+ * E <= 1024, top_k <= min(E, 64), T <= 2^24, T·top_k <= 2^30; in the products
+ * T·top_k·N and T·top_k·K <= 2^34.  T == 0 is a no-op but for offsets, which
+ * become zeros. */
 
 /* Workspace of an experts' call: GPTQ_WS_MOE (gptq_moe_route, gptq_moe_plan; N
  * and K unused), GPTQ_WS_EXPERT_GATED, GPTQ_WS_EXPERT_GEMM.  256 says that the
- * call uses none (NULL does as well).  Returns 0 for invalid arguments. */
+ * call uses none (NULL does as well).  Returns 0 for invalid arguments.  Its
+ * contents need not be kept between calls, nor cleared. */
 size_t gptq_expert_workspace_bytes(int which, int64_t T, int64_t top_k, int64_t n_experts, int64_t N,
                                    int64_t K);
 
@@ -595,7 +597,9 @@ int gptq_moe_plan(const int32_t* ids, int64_t T, int top_k, int64_t n_experts, i
  *                   ceil(K/128)].  U, u_scales, ldu, next_u: up weights.
  *  activation, C, c_dtype, ldc, codes, ld_codes, scales   as for
  *                   gptq_fp8_gated_gemm, T·top_k rows.
- *  ws               of GPTQ_WS_EXPERT_GATED. */
+ *  ws               NULL, or of GPTQ_WS_EXPERT_GATED: few tokens then share out
+ *                   the blocks of K (sums in another order than without, so
+ *                   results may differ in their rounding). */
 int gptq_fp8_expert_gated_gemm(const uint8_t* A, const float* a_scales, int64_t T, int64_t K,
                                int64_t lda, int top_k, const int32_t* offsets, const int32_t* order,
                                int64_t n_experts, const uint8_t* G, const float* g_scales,

@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 
 from . import _native
 
@@ -690,11 +691,16 @@ def rmsnorm_fp8(X, gamma, eps: float = 1e-6, residual=None, want_q: bool = True,
     return Normed(q, h, y)
 
 
+@functools.lru_cache(maxsize=4096)
+def _fp8_bytes(which, M, N, K):
+    return _native.lib().gptq_workspace_bytes(which, N, K, M, None)
+
+
 def _fp8_workspace(which, M, N, K, ws, dev):
     """(address, bytes, tensor to keep) of the split-K workspace; sizes that
     need none (the library says 256) get none."""
     if ws is None:
-        need = _native.lib().gptq_workspace_bytes(which, N, K, M, None)
+        need = _fp8_bytes(which, M, N, K)
         if need <= 256:
             return None, 0, None
         ws = _workspace(need, dev)
@@ -858,10 +864,15 @@ def expert_workspace_bytes(which: int, T: int, top_k: int, n_experts: int, N: in
     return int(_native.lib().gptq_expert_workspace_bytes(which, T, top_k, n_experts, N, K))
 
 
+@functools.lru_cache(maxsize=4096)
+def _expert_bytes(which, T, k, E, N, K):
+    return _native.lib().gptq_expert_workspace_bytes(which, T, k, E, N, K)
+
+
 def _expert_workspace(which, T, k, E, N, K, ws, dev):
     """(address, bytes, tensor to keep) of an experts' call's workspace."""
     if ws is None:
-        need = _native.lib().gptq_expert_workspace_bytes(which, T, k, E, N, K)
+        need = _expert_bytes(which, T, k, E, N, K)
         if need <= 256:
             return None, 0, None
         ws = _workspace(need, dev)

@@ -143,6 +143,13 @@ int check_slots(int64_t T, int64_t k, int64_t E) {
     return fail(GPTQ_ERR_INVALID_ARG, "T must be in [0, %lld] and T * top_k at most 2^30", (long long)kMaxDout);
   return GPTQ_OK;
 }
+// Rows of slots by the columns of either side: grids stay below 2^31 workgroups.
+int check_slot_size(int64_t T, int64_t k, int64_t N, int64_t K) {
+  const int64_t most = int64_t(1) << 34;
+  if (T * k * N > most || T * k * K > most)
+    return fail(GPTQ_ERR_INVALID_ARG, "T * top_k * N and T * top_k * K must be at most 2^34");
+  return GPTQ_OK;
+}
 int check_moe_ws(void* ws, size_t ws_bytes, int64_t T, int64_t E, int64_t k, const char* what) {
   const size_t need = gq::moe_ws_bytes(T, E, k);
   return ws || need > 256 ? check_ws(ws, ws_bytes, need, what) : GPTQ_OK;
@@ -699,8 +706,9 @@ size_t gptq_expert_workspace_bytes(int which, int64_t T, int64_t top_k, int64_t 
   if (which == GPTQ_WS_MOE) return gq::moe_ws_bytes(T, n_experts, top_k);
   if (which != GPTQ_WS_EXPERT_GATED && which != GPTQ_WS_EXPERT_GEMM) return 0;
   if (N <= 0 || N > kMaxDout || K <= 0 || K > kMaxDin) return 0;
+  if (check_slot_size(T, top_k, N, K)) return 0;
   if (T == 0) return 256;
-  return which == GPTQ_WS_EXPERT_GATED ? gq::fp8_expert_gated_ws_bytes()
+  return which == GPTQ_WS_EXPERT_GATED ? gq::fp8_expert_gated_ws_bytes(T, top_k, n_experts, N)
                                        : gq::fp8_expert_gemm_ws_bytes(T, top_k, N);
 }
 
@@ -769,6 +777,7 @@ int gptq_fp8_expert_gated_gemm(const uint8_t* A, const float* a_scales, int64_t 
   if (C && !valid_dtype(c_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown c_dtype %d", c_dtype);
   if (lda < K || ldg < K || ldu < K || (C && ldc < N) || (codes && ld_codes < N))
     return fail(GPTQ_ERR_INVALID_ARG, "a row stride is smaller than its row");
+  if ((rc = check_slot_size(T, top_k, N, K))) return rc;
   if (next_g < 0 || next_u < 0) return fail(GPTQ_ERR_INVALID_ARG, "next_g and next_u must be >= 0");
   if (T == 0) return GPTQ_OK;
   if (!A || !a_scales || !G || !g_scales || !U || !u_scales || !offsets || !order)
@@ -779,7 +788,7 @@ int gptq_fp8_expert_gated_gemm(const uint8_t* A, const float* a_scales, int64_t 
       misaligned(u_scales, GPTQ_F32) || misaligned(scales, GPTQ_F32) || misaligned(C, c_dtype) ||
       misaligned(offsets, GPTQ_F32) || misaligned(order, GPTQ_F32))
     return fail(GPTQ_ERR_INVALID_ARG, "a pointer is not aligned to its type");
-  const size_t need = gq::fp8_expert_gated_ws_bytes();
+  const size_t need = gq::fp8_expert_gated_ws_bytes(T, top_k, n_experts, N);
   if (ws && (rc = check_ws(ws, ws_bytes, need, "fp8_expert_gated_gemm"))) return rc;
   hipError_t e = gq::fp8_expert_gated_launch(A, a_scales, T, K, lda, top_k, offsets, order,
                                              (int)n_experts, G, g_scales, ldg, next_g, U, u_scales,
@@ -802,6 +811,7 @@ int gptq_fp8_expert_gemm(const uint8_t* H, const float* h_scales, int64_t T, int
   if (!valid_dtype(c_dtype)) return fail(GPTQ_ERR_INVALID_ARG, "unknown c_dtype %d", c_dtype);
   if (ldh < K || ldd < K || ldc < N || (R && ld_r < N))
     return fail(GPTQ_ERR_INVALID_ARG, "a row stride is smaller than its row");
+  if ((rc = check_slot_size(T, top_k, N, K))) return rc;
   if (next_d < 0) return fail(GPTQ_ERR_INVALID_ARG, "next_d must be >= 0");
   if (T == 0) return GPTQ_OK;
   if (!H || !h_scales || !D || !d_scales || !ids || !weights || !offsets || !order || !C)

@@ -218,7 +218,7 @@ hipError_t moe_route_launch(const void* X, int dt, int64_t T, int E, int64_t ld,
                             int32_t* offsets, int32_t* order, void* ws, hipStream_t s);
 hipError_t moe_plan_launch(const int32_t* ids, int64_t T, int k, int E, int32_t* offsets,
                            int32_t* order, void* ws, hipStream_t s);
-size_t fp8_expert_gated_ws_bytes();
+size_t fp8_expert_gated_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t N);
 size_t fp8_expert_gemm_ws_bytes(int64_t T, int64_t k, int64_t N);
 hipError_t fp8_expert_gated_launch(const uint8_t* A, const float* sa, int64_t T, int64_t K,
                                    int64_t lda, int k, const int32_t* offsets, const int32_t* order,

@@ -12,6 +12,8 @@
 // bf16 results these sums are rounded to fp16 on their way (kScaled): 2^-11 of
 // each term, an eighth of what the result's own rounding may lose, for half the
 // bytes (4096 tokens, top 8, 2048 columns: 227 -> 170 us).
+#include <cmath>
+
 #include "fp8_tile.hpp"
 
 namespace gq {
@@ -74,19 +76,30 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* P, int64_t nb,
 // row of H that this expert's product takes and its weight, or none.  A token
 // that has an expert twice gives that expert a second pass.  Copies as in
 // few_rows_kernel: each wave's own ring in LDS, its own waits.
-constexpr int kTokens = 16, kTokenSlots = 128, kTokenDepth = 3, kTokenWaves = 8;
+// Bound: the weights' bytes (top 2 of 8 experts of 4096 x 11008, one token: 18.8
+// us, 4.8 TB/s), with several tokens the waves' instructions beside them.  Us for
+// 1 / 4 / 16 tokens, in brackets the stream of 32-row tiles and the sum after it:
+//   top 8 of 64, 2048 x 1024      7.5 (15.5)   14.3 (19.9)   33.3 (31.4)
+//   top 2 of 8, 4096 x 11008     19.0 (54.6)   53.8 (73.7)   90.0 (97.7)
+//   top 8 of 256, 4096 x 512      7.7 (16.2)   15.1 (23.4)   42.6 (52.9)
+//   top 4 of 16, 1024 x 4096      9.0 (25.4)   16.6 (25.8)   25.0 (26.0)
+constexpr int kTokens = 16, kTokenSlots = 128;
 
-template <int NA> struct Token {
+// WAVES: 8, or 16 where there are few columns (16 tokens, top 4 of 16, 1024 x
+// 4096: 50.7 us with 8 and the addresses above, 25.0 with 16).
+template <int NA, int WAVES> struct Token {
   static constexpr int PER = 2 + NA + 1;                  // copies a block: B, A, scales
-  static constexpr int SLOT = 4096 + 256;                 // 16 rows of B, 16 of A; scales
-  static constexpr int RING = kTokenDepth * SLOT;
-  static constexpr int SMEM = kTokenWaves * RING;
+  static constexpr int DEPTH = WAVES == 16 ? 2 : 4;       // blocks in flight
+  static constexpr int SC = 2048 + NA * 1024;             // 16 rows of B, 8·NA of A; scales
+  static constexpr int SLOT = SC + 256;
+  static constexpr int RING = DEPTH * SLOT;
+  static constexpr int SMEM = WAVES * RING + (NA == 1 ? 1024 : 0);   // rows 8 to 15 of A: read, not used
 };
 
-template <int NA, bool FAST>
-__global__ __launch_bounds__(kTokenWaves * 64) void token_kernel(GArgs a, const int32_t* ids, const float* weights,
-                                                                  int tokens) {
-  using K = Token<NA>;
+template <int NA, bool FAST, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void token_kernel(GArgs a, const int32_t* ids, const float* weights,
+                                                           int tokens) {
+  using K = Token<NA, WAVES>;
   __shared__ __attribute__((aligned(1024))) char S[K::SMEM];
   __shared__ int expert_of[kTokenSlots], pass_of[kTokenSlots], token_of[kTokenSlots], again[kTokenSlots];
   __shared__ int pass_expert[kTokenSlots], passes_;
@@ -97,7 +110,7 @@ __global__ __launch_bounds__(kTokenWaves * 64) void token_kernel(GArgs a, const 
 
   // passes: the sorted positions' experts, and how often the token had each before
   const int live = offset_of(a, a.E);
-  for (int i = t; i < kTokenSlots * kTokens; i += kTokenWaves * 64) (&row_in[0][0])[i] = -1;
+  for (int i = t; i < kTokenSlots * kTokens; i += WAVES * 64) (&row_in[0][0])[i] = -1;
   if (t < kTokenSlots) {
     int e = -1, tok = 0;
     if (t < live) {
@@ -149,59 +162,84 @@ __global__ __launch_bounds__(kTokenWaves * 64) void token_kernel(GArgs a, const 
 
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int nleft = (int)min((int64_t)16, a.N - n0);
-  const int blocks = passes * a.kb, per = (blocks + kTokenWaves - 1) / kTokenWaves;
+  const int blocks = passes * a.kb, per = (blocks + WAVES - 1) / WAVES;
   const int begin = w * per, nblk = min(per, blocks - begin);   // may be 0 or less
   char* ring = S + w * K::RING;
   const unsigned rbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)ring;
-  const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;   // blocks from here on: through registers
-  // block j of this wave: pass and block of K
-  int cp = nblk > 0 ? begin / a.kb : 0, ck = nblk > 0 ? begin - cp * a.kb : 0;   // of the next copy
-  auto copy = [&](int j) {
-    const int slot = j % kTokenDepth;
+  // pass and block of K of the next copy, and what a pass has for it: the
+  // expert's weights and scales, each lane's row of H.  A pass's addresses are
+  // formed once: with new ones at every block the waves' instructions took
+  // longer than the bytes (8 tokens, top 1 of 8, 2048 x 4096: 17.7 us, now 11.8).
+  int cp = nblk > 0 ? begin / a.kb : 0, ck = nblk > 0 ? begin - cp * a.kb : 0;
+  const uint8_t* B = nullptr;
+  const float* scale = nullptr;
+  uint32_t boff[2], aoff[NA];
+  auto p16_of = [&](int i) { return (((lane & 7) ^ (lane >> 4)) << 4) ^ ((i & 1) << 6); };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) boff[i] = (uint32_t)min(i * 8 + (lane >> 3), nleft - 1) * (uint32_t)a.ldb[0] + p16_of(i);
+  auto turn = [&] {
     const int e = __builtin_amdgcn_readfirstlane(pass_expert[cp]);
-    const uint8_t* B = a.B[0] + e * a.next[0] + n0 * a.ldb[0];
-    i32x4 v[2 + NA];
+    B = a.B[0] + (int64_t)e * a.next[0] + n0 * a.ldb[0];
 #pragma unroll
-    for (int i = 0; i < 2 + NA; ++i) {
-      const int row = (i & 1) * 8 + (lane >> 3);
-      const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((i & 1) << 6);
-      const uint8_t* at = i < 2 ? B + (int64_t)min(row, nleft - 1) * a.ldb[0] : a.A + (int64_t)max((int)row_in[cp][row], 0) * a.lda;
-      if (ck < last_wide) lds_copy16(rbase + (unsigned)(slot * K::SLOT + i * 1024), at + (int64_t)ck * 128 + p16);
-      else v[i] = piece16(at, (int64_t)ck * 128 + p16, a.K);
-    }
-    {   // scales: lanes 0..15 the rows', the others the weights'
-      const float* p = lane < 16 ? a.sa + (int64_t)max((int)row_in[cp][l15], 0) * a.kb
-                                 : a.sb[0] + ((int64_t)e * a.nb + n0 / 128) * a.kb;
-      lds_copy4(rbase + (unsigned)(slot * K::SLOT + 4096), p + ck);
-    }
-    if (ck >= last_wide) {
+    for (int i = 0; i < NA; ++i) aoff[i] = (uint32_t)max((int)row_in[cp][i * 8 + (lane >> 3)], 0) * (uint32_t)a.lda + p16_of(i);
+    // lanes 0..15 the rows' scales, the others the weights'
+    scale = lane < 16 ? a.sa + (int64_t)max((int)row_in[cp][l15], 0) * a.kb
+                      : a.sb[0] + ((int64_t)e * a.nb + n0 / 128) * a.kb;
+  };
+  const int full = a.wide ? (int)(a.K / 128) : 0;   // blocks that are whole
+  auto copy = [&](int j) {
+    const unsigned to = (unsigned)((j % K::DEPTH) * K::SLOT);
+    const int64_t k = (int64_t)ck * 128;
+    if (ck < full) {
 #pragma unroll
-      for (int i = 0; i < 2 + NA; ++i) *reinterpret_cast<i32x4*>(ring + slot * K::SLOT + i * 1024 + lane * 16) = v[i];
+      for (int i = 0; i < 2; ++i) lds_copy16(rbase + to + i * 1024, B + k, boff[i]);
+#pragma unroll
+      for (int i = 0; i < NA; ++i) lds_copy16(rbase + to + 2048 + i * 1024, a.A + k, aoff[i]);
+      lds_copy4(rbase + to + K::SC, scale + ck);
+    } else if (a.wide && a.K % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) lds_copy16(rbase + to + i * 1024, within(B + k + boff[i], k + p16_of(i) < a.K));
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+        lds_copy16(rbase + to + 2048 + i * 1024, within(a.A + k + aoff[i], k + p16_of(i) < a.K));
+      lds_copy4(rbase + to + K::SC, scale + ck);
+    } else {   // through registers; rows at any stride
+      i32x4 v[2 + NA];
+#pragma unroll
+      for (int i = 0; i < 2 + NA; ++i) {
+        const int row = (i & 1) * 8 + (lane >> 3);
+        const uint8_t* at = i < 2 ? B + (int64_t)min(row, nleft - 1) * a.ldb[0] : a.A + (int64_t)max((int)row_in[cp][row], 0) * a.lda;
+        v[i] = piece16(at, k + p16_of(i), a.K);
+      }
+      lds_copy4(rbase + to + K::SC, scale + ck);
+#pragma unroll
+      for (int i = 0; i < 2 + NA; ++i) *reinterpret_cast<i32x4*>(ring + to + i * 1024 + lane * 16) = v[i];
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
     if (++ck == a.kb) {
       ck = 0;
-      ++cp;
+      if (++cp < passes) turn();
     }
   };
+  if (nblk > 0) turn();
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  int up = cp, uk = ck;   // pass and block of the next product
+  int up = cp, uk = ck;   // pass and block of the next product; whether the lane's token takes it
+  bool on = nblk > 0 && row_in[up][l15] >= 0;
+  float wt = nblk > 0 ? weight_in[up][l15] : 0.f;
 #pragma unroll
-  for (int j = 0; j < kTokenDepth; ++j)
+  for (int j = 0; j < K::DEPTH; ++j)
     if (j < nblk) copy(j);
   const int row = l15 * 128 + (((lane >> 4) ^ ((l15 >> 1) & 7)) << 4);
   for (int j = 0; j < nblk; ++j) {
     // this block's copies have landed when no more are in flight than the later blocks'
-    if (j + kTokenDepth <= nblk) asm volatile("s_waitcnt vmcnt(%0)" :: "i"((kTokenDepth - 1) * K::PER) : "memory");
+    if (j + K::DEPTH <= nblk) asm volatile("s_waitcnt vmcnt(%0)" :: "i"((K::DEPTH - 1) * K::PER) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    const char* q = ring + (j % kTokenDepth) * K::SLOT;
+    const char* q = ring + (j % K::DEPTH) * K::SLOT;
     const i32x4 bx = *reinterpret_cast<const i32x4*>(q + row), by = *reinterpret_cast<const i32x4*>(q + (row ^ 64));
     const i32x4 ax = *reinterpret_cast<const i32x4*>(q + 2048 + row), ay = *reinterpret_cast<const i32x4*>(q + 2048 + (row ^ 64));
-    const float sa = *reinterpret_cast<const float*>(q + 4096 + l15 * 4), sb = *reinterpret_cast<const float*>(q + 4096 + 64);
-    const bool on = row_in[up][l15] >= 0;
-    const float wt = weight_in[up][l15];
+    const float sa = *reinterpret_cast<const float*>(q + K::SC + l15 * 4), sb = *reinterpret_cast<const float*>(q + K::SC + 64);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read: the slot may be written again
-    if (j + kTokenDepth < nblk) copy(j + kTokenDepth);
+    if (j + K::DEPTH < nblk) copy(j + K::DEPTH);
     Frag<FAST> fb[1], fa;
     fb[0].set(bx, by);
     fa.set(ax, ay);
@@ -212,7 +250,10 @@ __global__ __launch_bounds__(kTokenWaves * 64) void token_kernel(GArgs a, const 
     for (int r = 0; r < 4; ++r) acc[r] = on ? __builtin_fmaf(p[0][r], s, acc[r]) : acc[r];
     if (++uk == a.kb) {
       uk = 0;
-      ++up;
+      if (++up < passes) {
+        on = row_in[up][l15] >= 0;
+        wt = weight_in[up][l15];
+      }
     }
   }
   __syncthreads();   // the sums go where the rings were
@@ -224,9 +265,565 @@ __global__ __launch_bounds__(kTokenWaves * 64) void token_kernel(GArgs a, const 
   if (m >= tokens || c >= nleft) return;
   float y = 0.f;
 #pragma unroll
-  for (int v = 0; v < kTokenWaves; ++v) y += part[(v * 16 + m) * 17 + c];
+  for (int v = 0; v < WAVES; ++v) y += part[(v * 16 + m) * 17 + c];
   if (a.R) y += get1(a.R, a.c_dt, m * a.ldr + n0 + c);
   put1(a.C, a.c_dt, m * a.ldc + n0 + c, y);
+}
+
+// ---------------------------------------------------------------- few gated columns
+// Gate and up for up to eight rows of one expert and 16 columns a workgroup, its
+// waves sharing out the blocks of K, each with a ring of its own in LDS: for few
+// tokens over few columns, where tiles of 128 columns leave most of the card idle.
+// Codes, one and two tokens (us, with the join's launch; in brackets the tiles and
+// their number): top 8 of 64 of 1024 x 2048 13.8 (16.3, 64), 20.9 (18.1, 120);
+// top 8 of 256 of 512 x 4096 15.4 (26.7, 32), 19.8 (28.4, 62); top 1 of 8 of 4096
+// x 2048 10.8 (16.1, 32), 14.6 (16.3, 60).
+// WAVES: 8, or 4 with two workgroups a CU where there are more than 256.
+template <int WAVES> struct FewGated {
+  static constexpr int PER = 4 + 1 + 1;                   // copies a block: gate, up, rows, scales
+  static constexpr int DEPTH = 3;
+  static constexpr int SC = 5 * 1024, SLOT = SC + 256;
+  static constexpr int RING = DEPTH * SLOT;
+  static constexpr int SMEM = WAVES * RING + 1024;        // rows 8 to 15: read, not used
+};
+
+template <bool FAST, int EPI, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void few_gated_kernel(GArgs a) {
+  using K = FewGated<WAVES>;
+  __shared__ __attribute__((aligned(1024))) char S[K::SMEM];
+  __shared__ int offs[kMaxExperts + 1];
+  const int t = threadIdx.x, lane = t & 63, l15 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  for (int e = t; e <= a.E; e += WAVES * 64) offs[e] = offset_of(a, e);
+  __syncthreads();
+  const uint32_t u = blockIdx.x / (uint32_t)a.tn;
+  const Stretches<8> all(offs, a.E);
+  if (u >= (uint32_t)all.total) return;
+  const int64_t n0 = (int64_t)(blockIdx.x - u * a.tn) * 16;
+  const Stretch s = all.find(offs, a.E, __builtin_amdgcn_readfirstlane((int)u));
+  const int nleft = (int)min((int64_t)16, a.N - n0);
+  // each lane's token for the copies of rows (eight lanes a row), and for those of scales
+  auto token = [&](int row) -> int {
+    const int o = a.order[s.row + min(row, s.rows - 1)];
+    return (unsigned)o < (unsigned)a.slots ? (int)((unsigned)o / (unsigned)a.topk) : 0;
+  };
+  const int mine = token(lane >> 3);
+  const uint8_t *G = a.B[0] + s.expert * a.next[0] + n0 * a.ldb[0], *U = a.B[1] + s.expert * a.next[1] + n0 * a.ldb[1];
+  const int64_t sb = ((int64_t)s.expert * a.nb + n0 / 128) * a.kb;
+  const float* scale = lane < 16 ? a.sa + (int64_t)token(l15) * a.kb : (lane < 32 ? a.sb[0] : a.sb[1]) + sb;
+  auto p16_of = [&](int i) { return (((lane & 7) ^ (lane >> 4)) << 4) ^ ((i & 1) << 6); };
+  uint32_t off[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    off[i] = (i < 4 ? (uint32_t)min((i & 1) * 8 + (lane >> 3), nleft - 1) * (uint32_t)a.ldb[i / 2 & 1]
+                    : (uint32_t)mine * (uint32_t)a.lda) + p16_of(i);
+  const int per = (a.kb + WAVES - 1) / WAVES, kbeg = w * per, nblk = min(per, a.kb - kbeg);   // may be 0 or less
+  char* ring = S + w * K::RING;
+  const unsigned rbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)ring;
+  const int full = a.wide ? (int)(a.K / 128) : 0;
+  auto copy = [&](int j) {
+    const unsigned to = (unsigned)((j % K::DEPTH) * K::SLOT);
+    const int64_t k = (int64_t)(kbeg + j) * 128;
+    if (kbeg + j < full) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) lds_copy16(rbase + to + i * 1024, (i < 2 ? G : i < 4 ? U : a.A) + k, off[i]);
+    } else if (a.wide && a.K % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i)
+        lds_copy16(rbase + to + i * 1024, within((i < 2 ? G : i < 4 ? U : a.A) + k + off[i], k + p16_of(i) < a.K));
+    } else {   // through registers; rows at any stride
+      i32x4 v[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const uint8_t* at = i < 4 ? (i < 2 ? G : U) + (int64_t)min((i & 1) * 8 + (lane >> 3), nleft - 1) * a.ldb[i / 2 & 1]
+                                  : a.A + (int64_t)mine * a.lda;
+        v[i] = piece16(at, k + p16_of(i), a.K);
+      }
+#pragma unroll
+      for (int i = 0; i < 5; ++i) *reinterpret_cast<i32x4*>(ring + to + i * 1024 + lane * 16) = v[i];
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    }
+    lds_copy4(rbase + to + K::SC, scale + kbeg + j);
+  };
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+  for (int j = 0; j < K::DEPTH; ++j)
+    if (j < nblk) copy(j);
+  const int row = l15 * 128 + (((lane >> 4) ^ ((l15 >> 1) & 7)) << 4);
+  for (int j = 0; j < nblk; ++j) {
+    // this block's copies have landed when no more are in flight than the later blocks'
+    if (j + K::DEPTH <= nblk) asm volatile("s_waitcnt vmcnt(%0)" :: "i"((K::DEPTH - 1) * K::PER) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const char* q = ring + (j % K::DEPTH) * K::SLOT;
+    i32x4 x[3], y[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      x[i] = *reinterpret_cast<const i32x4*>(q + i * 2048 + row);
+      y[i] = *reinterpret_cast<const i32x4*>(q + i * 2048 + (row ^ 64));
+    }
+    const float* sc = reinterpret_cast<const float*>(q + K::SC);
+    const float sa = sc[l15], sg = sc[16], su = sc[32];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read: the slot may be written again
+    if (j + K::DEPTH < nblk) copy(j + K::DEPTH);
+    Frag<FAST> fb[2], fa;
+    fb[0].set(x[0], y[0]);
+    fb[1].set(x[1], y[1]);
+    fa.set(x[2], y[2]);
+    f32x4 p[2];
+    contract(fb, fa, p);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      acc[0][r] = __builtin_fmaf(p[0][r], sa * sg, acc[0][r]);
+      acc[1][r] = __builtin_fmaf(p[1][r], sa * su, acc[1][r]);
+    }
+  }
+  __syncthreads();   // the sums go where the rings were
+  float* part = reinterpret_cast<float*>(S);
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) part[((w * 2 + b) * 16 + l15) * 17 + 4 * (lane >> 4) + r] = acc[b][r];
+  __syncthreads();
+  const int m = t >> 4, c = t & 15;
+  if (m >= s.rows || c >= nleft) return;
+  float g = 0.f, h = 0.f;
+#pragma unroll
+  for (int v = 0; v < WAVES; ++v) {
+    g += part[(v * 2 * 16 + m) * 17 + c];
+    h += part[((v * 2 + 1) * 16 + m) * 17 + c];
+  }
+  h *= activate(g, a.act);
+  const int64_t at = s.row + m;
+  if constexpr (EPI == kPartial) a.P[at * a.N + n0 + c] = h;
+  else put1(a.C, a.c_dt, at * a.ldc + n0 + c, h);
+}
+
+// ---------------------------------------------------------------- stream of tiles
+// The tile kernel's loop (fp8_tile.hpp) over many tiles a workgroup, as one
+// stream of stages: while a tile's last stages are multiplied the first ones of
+// the workgroup's next tile are copied, so that a tile costs its stages and its
+// stores, and not the way there (finding the expert, its rows, the first bytes)
+// that a workgroup of its own would wait for.  The products of a token's slots
+// back are short (8 stages for 1024 columns).
+// The slots of a tile's rows come with copies of 4 bytes a lane like the scales;
+// three tables of them, for the wave that still stores the tile before, this
+// tile and the next.
+// FLOW: that; otherwise one tile a workgroup.  A stage of a stream is up to a
+// tenth slower (more scalars than there are registers for), so long products go
+// without: 4096 x 11008 over 8 experts of 1024 rows 519 us without, 550 with it;
+// 4096 x 512 over 256 experts of 32 rows 199 and 172, of 128 rows 398 and 322.
+template <int BM, int BN, int WM, int WN, int NS, int EPI, bool FLOW> struct Stream {
+  using T = Tile<BM, BN, WM, WN, NS>;
+  static constexpr int ROWS = BM < 64 ? 64 : BM;   // of a table: a copy fills 64
+  static constexpr int TOP = EPI == kCodes ? BN / WN * BM : 1;
+  static constexpr int TABLES = FLOW ? 3 : 1;
+  static constexpr int LDS = T::SMEM + 4 * (kMaxExperts + 1 + TABLES * ROWS + TOP) + 64;
+  static constexpr int FIT = 163840 / LDS;         // workgroups a CU
+  static_assert(FIT >= 1, "LDS");
+  static constexpr int WPE = FIT * T::WAVES / 4 > 8 ? 8 : FIT * T::WAVES / 4;
+};
+
+template <int BM, int BN, int WM, int WN, int NS, bool FAST, int FORM, int EPI, int DT, int ROWS, bool FLOW>
+__global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Stream<BM, BN, WM, WN, NS, EPI, FLOW>::WPE)) void stream_kernel(GArgs a) {
+  using T = Tile<BM, BN, WM, WN, NS>;
+  using Q = Stream<BM, BN, WM, WN, NS, EPI, FLOW>;
+  constexpr bool GATED = FORM == kGated;
+  constexpr int MI = T::MI, NI = T::NI, NB = GATED ? 2 : 1;
+  constexpr int G = !FAST && MI * NI < 32 && NI % 2 == 0 ? 2 : 1;
+  constexpr int FIRST = FAST && MI * NI == 32 ? T::PER / 2 : T::PER;
+  constexpr int BC = BN / NB, WC = WN / NB;
+  __shared__ __attribute__((aligned(1024))) char S[T::SMEM];
+  __shared__ int offs[kMaxExperts + 1];
+  __shared__ int slots_[Q::TABLES][Q::ROWS];
+  __shared__ uint32_t top[Q::TOP];
+  const int t = threadIdx.x, lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = w / (BN / WN), wn = w % (BN / WN);
+  for (int e = t; e <= a.E; e += T::NT) offs[e] = offset_of(a, e);
+  __syncthreads();
+  const Stretches<BM> all(offs, a.E);
+  const uint32_t tiles = (uint32_t)all.total * a.tn;
+  if (blockIdx.x >= tiles) return;
+  struct Where { int e, m0, mleft, n0; };
+  auto where = [&](uint32_t L) -> Where {
+    uint32_t bm, bn;
+    tile_of(L, tiles, all.total, a.tn, bm, bn);
+    const Stretch s = all.find(offs, a.E, __builtin_amdgcn_readfirstlane((int)bm));
+    return {s.expert, s.row, s.rows, __builtin_amdgcn_readfirstlane((int)bn * BC)};
+  };
+  const int nst = a.kb;
+  const bool flow = FLOW && nst > NS;   // enough stages for the next tile's tables to arrive
+  const unsigned sbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)S;
+  const unsigned tbase = (unsigned)(uintptr_t)(__attribute__((address_space(3))) int*)&slots_[0][0];
+  const int last_wide = a.wide ? (a.K % 128 ? a.kb - 1 : a.kb) : 0;
+
+  auto copy_slots = [&](const Where& p, int b) {
+#pragma unroll
+    for (int i = w; i < Q::ROWS / 64; i += T::WAVES)
+      lds_copy4(tbase + (unsigned)(b * Q::ROWS * 4 + i * 256), a.order + p.m0 + min(i * 64 + lane, p.mleft - 1));
+  };
+  auto token = [&](int b, int row) -> int {   // of a tile's row; a slot that does not exist: any
+    const int o = slots_[b][row];
+    return (unsigned)o < (unsigned)a.slots ? (int)((unsigned)o / (unsigned)a.topk) : 0;
+  };
+  auto copy_scales = [&](const Where& p, int b, int g, int half) {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    const int r = l >> 3, k = min(8 * g + (l & 7), a.kb - 1);
+#pragma unroll 1
+    for (int idx = w; idx < T::SCOPIES; idx += T::WAVES) {
+      const float* q;
+      if (idx < BM / 8) {
+        const int64_t row = ROWS == kGather ? (int64_t)token(b, idx * 8 + r) : (int64_t)p.m0 + min(idx * 8 + r, p.mleft - 1);
+        q = a.sa + row * a.kb;
+      } else {
+        const int64_t blk = (int64_t)p.e * a.nb + p.n0 / 128;
+        if (GATED) q = (r == 0 ? a.sb[0] : a.sb[NB - 1]) + blk * a.kb;
+        else q = a.sb[0] + (blk + min(min(r, 1), (int)a.nb - 1 - p.n0 / 128)) * a.kb;
+      }
+      lds_copy4(sbase + T::SCALES + (unsigned)((half & 1) * T::SCB + idx * 256), q + k);
+    }
+  };
+  // where the copies of stages are: bases and the lanes' offsets
+  const uint8_t *base_a = nullptr, *base_b = nullptr, *base_u = nullptr;
+  uint32_t voff[T::PER];
+  Where from{};   // the tile that is copied, and its table
+  int from_tab = 0;
+  auto copy_from = [&](const Where& p, int b) {
+    from = p;
+    from_tab = b;
+    base_a = ROWS == kGather ? a.A : a.A + (int64_t)p.m0 * a.lda;
+    base_b = a.B[0] + (int64_t)p.e * a.next[0] + (int64_t)p.n0 * a.ldb[0];
+    if constexpr (GATED) base_u = a.B[1] + (int64_t)p.e * a.next[1] + (int64_t)p.n0 * a.ldb[1];
+    const int nleft = (int)min((int64_t)BC, a.N - p.n0);
+    int l = lane;
+    asm volatile("" : "+v"(l));   // once a tile: not worth registers
+#pragma unroll
+    for (int i = 0; i < T::PER; ++i) {
+      const int seg = T::seg(w, i), row = seg * 8 + (l >> 3);
+      const int p16 = (((l & 7) ^ (l >> 4)) << 4) ^ ((seg & 1) << 6);
+      if (seg < BM / 8) {
+        voff[i] = (uint32_t)(ROWS == kGather ? token(b, row) : min(row, p.mleft - 1)) * (uint32_t)a.lda + p16;
+      } else {
+        const int half = GATED && seg >= (BM + BC) / 8;
+        voff[i] = (uint32_t)min(row - BM - half * BC, nleft - 1) * (uint32_t)a.ldb[half] + p16;
+      }
+    }
+  };
+  auto seg_base = [&](int seg) { return seg < BM / 8 ? base_a : GATED && seg >= (BM + BC) / 8 ? base_u : base_b; };
+  // copies i0 .. i1 - 1 of block st of K, into the ring's stage n
+  auto copy = [&](int st, int n, int i0, int i1) {
+    const unsigned buf = (unsigned)((n % NS) * T::SB);
+    if (st < last_wide) {
+#pragma unroll
+      for (int i = i0; i < i1; ++i) {
+        const int seg = T::seg(w, i);
+        lds_copy16(sbase + buf + (unsigned)seg * 1024u, seg_base(seg) + (int64_t)st * 128, voff[i]);
+      }
+    } else if (a.wide && a.K % 16 == 0) {   // a last block that K cuts between two pieces
+#pragma unroll
+      for (int i = i0; i < i1; ++i) {
+        const int seg = T::seg(w, i);
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        const int p16 = (((l & 7) ^ (l >> 4)) << 4) ^ ((seg & 1) << 6);
+        lds_copy16(sbase + buf + (unsigned)seg * 1024u,
+                   within(seg_base(seg) + voff[i] + (int64_t)st * 128, st * 128 + p16 < a.K));
+      }
+    } else if (i0 == 0) {   // through registers; offsets of rows at any stride, in 64 bits
+#pragma unroll 1
+      for (int i = 0; i < T::PER; ++i) {
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        const int seg = T::seg(w, i), row = seg * 8 + (l >> 3);
+        const int p16 = (((l & 7) ^ (l >> 4)) << 4) ^ ((seg & 1) << 6);
+        const uint8_t* q;
+        if (seg < BM / 8) {
+          const int r = ROWS == kGather ? token(from_tab, row) : min(row, from.mleft - 1);
+          q = base_a + (int64_t)r * a.lda;
+        } else {
+          const int half = GATED && seg >= (BM + BC) / 8;
+          q = (half ? base_u : base_b) + (int64_t)min(row - BM - half * BC, (int)min((int64_t)BC, a.N - from.n0) - 1) * a.ldb[half];
+        }
+        *reinterpret_cast<i32x4*>(S + buf + seg * 1024 + l * 16) = piece16(q, (int64_t)st * 128 + p16, a.K);
+      }
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    }
+  };
+
+  f32x4 acc[NI][MI];
+  const int l15 = lane & 15, sw = ((lane >> 4) ^ ((l15 >> 1) & 7)) << 4;
+  const int arow = (wm * WM + l15) * 128 + sw;
+  const int brow = (BM + wn * WC + l15) * 128 + sw;
+  const int soff = T::SCALES + (wm * WM + l15) * 32;
+  const int boff = T::SCALES + BM * 32 + (GATED ? 0 : wn * WC / 128 * 32);
+  struct Raw { i32x4 x, y; };
+  auto read_b = [&](const char* b, int j) -> Raw {
+    const int off = brow + (GATED ? (j / (NI / 2)) * BC * 128 + (j % (NI / 2)) * 2048 : j * 2048);
+    return {*reinterpret_cast<const i32x4*>(b + off), *reinterpret_cast<const i32x4*>(b + (off ^ 64))};
+  };
+  auto read_a = [&](const char* b, int i) -> Raw {
+    const int off = arow + i * 2048;
+    return {*reinterpret_cast<const i32x4*>(b + off), *reinterpret_cast<const i32x4*>(b + (off ^ 64))};
+  };
+
+  uint32_t L = blockIdx.x;
+  Where cur = where(L), next = cur;
+  int ring = 0, half = 0, tab = 0;   // stages, groups of scales and tables before this tile (mod NS, 2, 3)
+  bool fresh = true, ready = false;  // no copies are under way; the first pieces are in registers
+  const int groups = (nst + 7) >> 3;
+  // the stage at which the next tile's first scales are asked for: when their
+  // buffer is free, and with its first stage if that is later
+  const int ask = max(8 * (groups - 1), nst - NS + 1);
+  Frag<FAST> fb[NI], fa;
+  Raw ra;
+  float sb[NB], sa, sn;
+  for (;;) {
+    const bool last = !FLOW || L + gridDim.x >= tiles;
+    if (!last) next = where(L + gridDim.x);
+    const bool more = flow && !last;
+    const int tab2 = tab == 2 ? 0 : tab + 1;
+    if (fresh) {
+      copy_slots(cur, tab);
+      if constexpr (ROWS == kGather) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      copy_from(cur, tab);
+      copy_scales(cur, tab, 0, half);
+      for (int s0 = 0; s0 < NS - 1 && s0 < nst; ++s0) copy(s0, ring + s0, 0, T::PER);
+      stage_barrier<T::PER>(min(nst - 1, NS - 2));
+      ready = false;
+    }
+    if (more) copy_slots(next, tab2);
+    // what stage st asks for: the first copies, scales; then the others
+    auto ask_for = [&](int st) {
+      const int c = st + NS - 1;
+      if (c == nst && more) copy_from(next, tab2);
+      if (more && st == ask) copy_scales(next, tab2, 0, half + groups);
+      if (c < nst) copy(c, ring + c, 0, FIRST);
+      else if (more) copy(c - nst, ring + c, 0, FIRST);
+      if ((st & 7) == 0 && st + 8 < nst) copy_scales(cur, tab, (st >> 3) + 1, half + (st >> 3) + 1);
+    };
+    auto ask_rest = [&](int st) {
+      const int c = st + NS - 1;
+      if (c < nst) copy(c, ring + c, FIRST, T::PER);
+      else if (more) copy(c - nst, ring + c, FIRST, T::PER);
+    };
+    // the copies that may be in flight behind stage st: none of those that the
+    // next tile's first stage reads
+    auto ahead = [&](int st) {
+      if (!more) return min(nst - 1, st + NS - 1) - (st + 1);
+      return st == nst - 1 && ask > nst - NS + 1 ? 0 : NS - 2;
+    };
+    const bool idle = wm * WM >= cur.mleft;   // none of the wave's rows exist: copies only
+    if (idle) {
+      for (int st = 0; st < nst; ++st) {
+        ask_for(st);
+        if (FIRST < T::PER) ask_rest(st);
+        stage_barrier<T::PER>(ahead(st));
+      }
+      ready = false;
+    } else {
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int i = 0; i < MI; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      float ssum[EPI == kScaled ? MI : 1];   // Σ|sa·sb| of each A piece's row
+      if constexpr (EPI == kScaled) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) ssum[i] = 0.f;
+      }
+      if (!ready) {
+        const char* b = S + (ring % NS) * T::SB;
+        const char* sc = S + (half & 1) * T::SCB;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) { const Raw r = read_b(b, j); fb[j].set(r.x, r.y); }
+        ra = read_a(b, 0);
+        sn = *reinterpret_cast<const float*>(sc + soff);
+#pragma unroll
+        for (int q = 0; q < NB; ++q) sb[q] = *reinterpret_cast<const float*>(sc + boff + 32 * q);
+      }
+      for (int st = 0; st < nst; ++st) {
+        ask_for(st);
+        const char* sc = S + ((half + (st >> 3)) & 1) * T::SCB + (st & 7) * 4;
+        const char* sc_ = st + 1 < nst ? S + ((half + ((st + 1) >> 3)) & 1) * T::SCB + ((st + 1) & 7) * 4
+                                       : S + ((half + groups) & 1) * T::SCB;
+        const char* b = S + ((ring + st) % NS) * T::SB;
+        const char* bn_ = S + ((ring + st + 1) % NS) * T::SB;
+        f32x4 p[G];
+        float sp[G] = {}, s[NB];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          if (i == 1 && FIRST < T::PER) ask_rest(st);
+          fa.set(ra.x, ra.y);
+          sa = sn;
+#pragma unroll
+          for (int q = 0; q < NB; ++q) s[q] = sa * sb[q];
+          if constexpr (EPI == kScaled) ssum[i] += fabsf(s[0]);
+          if (i + 1 < MI) {
+            ra = read_a(b, i + 1);
+            sn = *reinterpret_cast<const float*>(sc + soff + (i + 1) * 512);
+          } else {
+            stage_barrier<T::PER>(ahead(st));
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int j = 0; j < NI; j += G) {
+            f32x4 q[G];
+            contract(&fb[j], fa, q);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              if (i + j > 0) asm volatile("" : "+v"(q[g]), "+v"(p[g]));
+              else asm volatile("" : "+v"(q[g]));
+            }
+            if (i + 1 == MI) {   // the next stage's pieces (where there is none: unused bytes)
+#pragma unroll
+              for (int g = 0; g < G; ++g) {
+                const Raw r = read_b(bn_, j + g);
+                fb[j + g].set(r.x, r.y);
+              }
+              if (j == 0) {
+                ra = read_a(bn_, 0);
+                sn = *reinterpret_cast<const float*>(sc_ + soff);
+#pragma unroll
+                for (int h = 0; h < NB; ++h) sb[h] = *reinterpret_cast<const float*>(sc_ + boff + 32 * h);
+              }
+            }
+            const int pi = j > 0 ? i : i - 1, pj = j > 0 ? j - G : NI - G;
+            if (pi >= 0) {
+#pragma unroll
+              for (int g = 0; g < G; ++g) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  acc[pj + g][pi][r] = __builtin_fmaf(p[g][r], sp[g], acc[pj + g][pi][r]);
+                asm volatile("" : "+v"(acc[pj + g][pi]));
+              }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              p[g] = q[g];
+              sp[g] = s[GATED ? (j + g) / (NI / 2) : 0];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[NI - G + g][MI - 1][r] = __builtin_fmaf(p[g][r], sp[g], acc[NI - G + g][MI - 1][r]);
+      }
+      ready = more;
+      const int nleft = (int)min((int64_t)BC, a.N - cur.n0);
+      int l = lane;
+      asm volatile("" : "+v"(l));
+      const int l15 = l & 15, nl = wn * WC + 4 * (l >> 4);   // this lane's first column in the tile
+      constexpr int NO = GATED ? NI / 2 : NI;
+      if constexpr (EPI == kPartial || EPI == kScaled) {
+        // kScaled: P is fp16 [slots][N], behind it the powers of two [slots][nb]
+        _Float16* P = reinterpret_cast<_Float16*>(a.P);
+        float* F = reinterpret_cast<float*>(P + align_scaled((int64_t)a.slots * a.N));
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const int ml = wm * WM + i * 16 + l15;
+          const int64_t row = slots_[tab][ml];
+          if (ml >= cur.mleft || row < 0 || row >= a.slots) continue;
+          if constexpr (EPI == kScaled) {
+            const int e = scaled_exponent(ssum[i]);
+            const float f = power_of_two(-e);
+            if (lane < 16 && (wn * WC) % 128 == 0 && nl < nleft) F[row * a.nb + (cur.n0 + nl) / 128] = power_of_two(e);
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[j][i][r] *= f;
+              put4<GPTQ_F16>(P, row * a.N + cur.n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+              put4<GPTQ_F32>(a.P, row * a.N + cur.n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+          }
+        }
+      } else {
+        const Activation act(a.act);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < NO; ++j) {
+            acc[j][i] = act(acc[j][i]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[j][i][r] *= acc[NO + j][i][r];
+          }
+        if constexpr (EPI == kStore) {
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            const int ml = wm * WM + i * 16 + l15;
+            if (ml >= cur.mleft) continue;
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+              put4<DT>(a.C, ((int64_t)cur.m0 + ml) * a.ldc + cur.n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+          }
+        }
+      }
+    }
+    if constexpr (EPI == kCodes) {
+      // the tile's 128 columns are one block of its rows
+      static_assert(EPI != kCodes || BC == 128, "a tile is one block wide");
+      constexpr int NO = NI / 2;
+      const int nleft = (int)min((int64_t)BC, a.N - cur.n0);
+      int l = lane;
+      asm volatile("" : "+v"(l));
+      const int l15 = l & 15, nl = wn * WC + 4 * (l >> 4);
+      if (!idle) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          uint32_t u = 0;
+#pragma unroll
+          for (int j = 0; j < NO; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (nl + j * 16 + r < nleft) u = max(u, mag_bits(acc[j][i][r]));
+          u = max(u, (uint32_t)__shfl_xor((int)u, 16));
+          u = max(u, (uint32_t)__shfl_xor((int)u, 32));
+          if (lane < 16) top[wn * BM + wm * WM + i * 16 + l15] = u;
+        }
+      }
+      // without waiting for the copies under way
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (!idle) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const int ml = wm * WM + i * 16 + l15;
+          uint32_t u = 0;
+#pragma unroll
+          for (int q = 0; q < BN / WN; ++q) u = max(u, top[q * BM + ml]);
+          const float s = e4m3_scale((double)__builtin_bit_cast(float, u));
+          const float inv = 1.f / s;
+          if (ml >= cur.mleft) continue;
+          const int64_t row = (int64_t)cur.m0 + ml;
+          if (wn == 0 && lane < 16) a.sc[row * a.nb + cur.n0 / 128] = s;
+#pragma unroll
+          for (int j = 0; j < NO; ++j) {
+            const uint32_t c = codes4(acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3], s, inv);
+            uint8_t* o = a.codes + row * a.ld_codes + cur.n0 + nl + j * 16;
+            const int n = nleft - nl - j * 16;
+            if (n >= 4) {
+              __builtin_memcpy(o, &c, 4);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (r < n) o[r] = (uint8_t)(c >> (8 * r));
+            }
+          }
+        }
+      }
+    }
+    if (last) break;
+    L += gridDim.x;
+    cur = next;
+    ring = (ring + nst) % NS;
+    half = (half + groups) & 1;
+    tab = tab2;
+    fresh = !flow;
+  }
 }
 
 // ---------------------------------------------------------------- launch
@@ -235,13 +832,15 @@ int64_t most_stretches(int64_t slots, int64_t E, int64_t bm) {
   return std::min(slots, slots / bm + std::min(E, slots));
 }
 
-template <int BM, int BN, int WM, int WN, int NS, bool FAST, int FORM, int EPI, int DT, int ROWS>
-hipError_t launch_tile(GArgs& a, hipStream_t s) {
-  using T = Tile<BM, BN, WM, WN, NS>;
+template <int BM, int BN, int WM, int WN, int NS, bool FAST, int FORM, int EPI, int DT, int ROWS, bool FLOW = false>
+hipError_t launch_tiles(GArgs& a, hipStream_t s) {
   a.tn = (int)ceil_div(a.N, FORM == kGated ? BN / 2 : BN);
-  const int64_t grid = most_stretches(a.slots, a.E, BM) * a.tn;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  tile_kernel<BM, BN, WM, WN, NS, FAST, FORM, EPI, DT, ROWS><<<(unsigned)grid, T::NT, 0, s>>>(a);
+  const int64_t most = most_stretches(a.slots, a.E, BM) * a.tn;
+  if (most > INT32_MAX) return hipErrorInvalidValue;
+  // FLOW: as many workgroups as run at once (a multiple of 8: each stays with its XCD's tiles)
+  const unsigned grid = (unsigned)(FLOW ? std::min<int64_t>(most, 256 * Stream<BM, BN, WM, WN, NS, EPI, FLOW>::FIT) : most);
+  stream_kernel<BM, BN, WM, WN, NS, FAST, FORM, EPI, DT, ROWS, FLOW>
+      <<<grid, Tile<BM, BN, WM, WN, NS>::NT, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -257,6 +856,14 @@ bool wide_rows(const uint8_t* q, int64_t rows, int64_t ld, int64_t most) {
 // Rows of an expert, on average over those that can have any.
 double rows_each(const GArgs& a) { return (double)a.slots / (double)std::min(a.slots, a.E); }
 
+// Whether tiles of 128 columns would leave most of the card idle: their number,
+// from the experts that so many tokens take if they like all alike.
+bool few_gated(int64_t slots, int64_t E, int64_t k, int64_t N) {
+  if (slots > 64) return false;
+  const double hit = E * (1.0 - std::pow(1.0 - (double)k / E, (double)(slots / k)));
+  return hit * ceil_div(N, 128) < 80;
+}
+
 // Tiles by the rows an expert has.  Up to 32 rows all of them wait for the
 // weights and the smallest tile that holds most experts' rows is best: a second
 // one reads the weights again, if only from the L2; above, the products count.
@@ -264,32 +871,60 @@ double rows_each(const GArgs& a) { return (double)a.slots / (double)std::min(a.s
 //   rows        2 / 1         8 / 16        32 / 64       128 / 256     512 / 1024
 //   16 x 256    48.9 / 116.7  67.0 / 191.1  92.8 / 360    288 / 1199    954 / 4597
 //   32 x 256    51.9 / 119.1  60.3 / 164.3  70.9 / 263    189 / 723     594 / 2727
+//   64 x 256    57.2 / 131.7  58.3 / 167.0  86.1 / 239    137 / 533     424 / 1933
 //   128 x 256   73.3 / 166.2  67.5 / 188.8  79.6 / 209    116 / 455     320 / 1469
 //   256 x 256   127 / 279     103 / 257     99 / 259      177 / 469     326 / 1493
+// Bound, from 128 rows on: issue.  The exact form converts both operands in
+// every wave, two conversions for each product of a 64 x 64 wave, and adds each
+// block's sums; 8 experts of 1024 rows run at 1.0 PFLOP/s.
 template <int EPI, int DT> hipError_t run_gated(GArgs& a, hipStream_t s) {
   constexpr bool FAST = EPI == kStore && DT != GPTQ_F32;
   const double r = rows_each(a);
-  if (r < 6) return launch_tile<16, 256, 16, 32, 4, FAST, kGated, EPI, DT, kGather>(a, s);
-  if (r < 48) return launch_tile<32, 256, 32, 32, 4, FAST, kGated, EPI, DT, kGather>(a, s);
-  return launch_tile<128, 256, 64, 64, 2, FAST, kGated, EPI, DT, kGather>(a, s);
+  if (few_gated(a.slots, a.E, a.topk, a.N) && (EPI != kCodes || a.P)) {
+    constexpr int E = EPI == kCodes ? kPartial : kStore;
+    a.tn = (int)ceil_div(a.N, 16);
+    const unsigned grid = (unsigned)(most_stretches(a.slots, a.E, 8) * a.tn);
+    if (grid <= 256) few_gated_kernel<FAST, E, 8><<<grid, 512, 0, s>>>(a);
+    else few_gated_kernel<FAST, E, 4><<<grid, 256, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || EPI != kCodes) return e;
+    join_kernel<kPlain, true, kGather><<<(unsigned)ceil_div(a.M * a.nb, 16), 256, 0, s>>>(a, 1);
+    return hipGetLastError();
+  }
+  if (r < 6) return launch_tiles<16, 256, 16, 32, 4, FAST, kGated, EPI, DT, kGather>(a, s);
+  if (r < 48) return launch_tiles<32, 256, 32, 32, 4, FAST, kGated, EPI, DT, kGather>(a, s);
+  return launch_tiles<128, 256, 64, 64, 2, FAST, kGated, EPI, DT, kGather>(a, s);
 }
-// Back, to bf16 with the sum over the slots (2048 x 1024 / 4096 x 11008):
-//   rows        2 / 4         8 / 16        32 / 64       128 / 256     512 / 1024
-//   16 x 128    25.6 / 112.8  37.7 / 117    45.3 / 197    117 / 454     381 / 1554
-//   32 x 128    26.8 / 95.2   33.7 / 98.1   41.2 / 136    95.4 / 293    307 / 1004
-//   128 x 128   29.5 / 114.4  35.1 / 111    40.9 / 123    67.1 / 219    191 / 532
-//   256 x 256   39.6 / 150.7  39.3 / 148    45.3 / 154    81.0 / 198    170 / 519
+// Back, to bf16 with the sum over the slots (streams; us; 64 experts of 2048 x
+// 1024, top 8 / 256 of 4096 x 512, top 8):
+//   rows        8 / 2         32 / 8        128 / 32      512 / 128
+//   16 x 128    34.6 / 97     48.6 / 124    122 / 204     403 / 608
+//   32 x 128    32.1 / 99     38.0 / 125    86 / 177      276 / 437
+//   64 x 128    35.4 / 113    46.5 / 144    89 / 200      274 / 465
+//   128 x 128   35.7 / 110    42.6 / 142    68 / 185      189 / 344
+//   128 x 256   33.4 / 98     40.8 / 125    63 / 172      177 / 322
+//   256 x 256   39.6 / 121    45.3 / 151    87 / 200      167 / 367
+// (exact 256-row tiles have no registers left).  Bound: at few rows the weights'
+// bytes, at many the stores of the terms, which a tile's last stages wait for.
 template <bool FAST, int EPI> hipError_t run_sorted(GArgs& a, hipStream_t s) {
   const double r = rows_each(a);
-  if (r < 4) return launch_tile<16, 128, 16, 32, 2, FAST, kPlain, EPI, GPTQ_F32, kSorted>(a, s);
-  if (r < 48) return launch_tile<32, 128, 32, 32, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted>(a, s);
-  if (r < 200) return launch_tile<128, 128, 64, 32, 2, FAST, kPlain, EPI, GPTQ_F32, kSorted>(a, s);
-  return launch_tile<256, 256, 128, 64, 2, FAST, kPlain, EPI, GPTQ_F32, kSorted>(a, s);
+  if (r < 48) return launch_tiles<32, 128, 32, 32, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, true>(a, s);
+  if (!FAST || r < 300) {
+    if (a.kb > 20) return launch_tiles<128, 256, 64, 64, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, false>(a, s);
+    return launch_tiles<128, 256, 64, 64, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, true>(a, s);
+  }
+  if constexpr (FAST) {
+    if (a.kb > 20) return launch_tiles<256, 256, 128, 64, 2, FAST, kPlain, EPI, GPTQ_F32, kSorted, false>(a, s);
+    return launch_tiles<256, 256, 128, 64, 2, FAST, kPlain, EPI, GPTQ_F32, kSorted, true>(a, s);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t fp8_expert_gated_ws_bytes() { return 256; }   // none
+size_t fp8_expert_gated_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t N) {
+  return few_gated(T * k, E, k, N) ? std::max<size_t>(512, align_up((size_t)(T * k) * N * 4)) : 256;
+}
 size_t fp8_expert_gemm_ws_bytes(int64_t T, int64_t k, int64_t N) {
   if (T <= kTokens && T * k <= kTokenSlots) return 256;
   return std::max<size_t>(512, align_up((size_t)(T * k) * N * 4));
@@ -335,14 +970,18 @@ hipError_t fp8_expert_gemm_launch(const uint8_t* A, const float* sa, int64_t T, 
   a.R = R; a.ldr = ldr; a.C = C; a.c_dt = c_dt; a.ldc = ldc;
   if (T <= kTokens && T * k <= kTokenSlots) {
     const unsigned grid = (unsigned)ceil_div(N, 16);
-#define GQ_TOKEN(NA, FAST) token_kernel<NA, FAST><<<grid, kTokenWaves * 64, 0, s>>>(a, ids, weights, (int)T)
-    if (c_dt == GPTQ_F32) {
-      if (T <= 8) GQ_TOKEN(1, false);
-      else GQ_TOKEN(2, false);
-    } else {
-      if (T <= 8) GQ_TOKEN(1, true);
-      else GQ_TOKEN(2, true);
-    }
+#define GQ_TOKEN(NA, FAST, W) token_kernel<NA, FAST, W><<<grid, W * 64, 0, s>>>(a, ids, weights, (int)T)
+#define GQ_TOKENS(FAST) \
+  do { \
+    if (grid <= 128) { \
+      if (T <= 8) GQ_TOKEN(1, FAST, 16); \
+      else GQ_TOKEN(2, FAST, 16); \
+    } else if (T <= 8) GQ_TOKEN(1, FAST, 8); \
+    else GQ_TOKEN(2, FAST, 8); \
+  } while (0)
+    if (c_dt == GPTQ_F32) GQ_TOKENS(false);
+    else GQ_TOKENS(true);
+#undef GQ_TOKENS
 #undef GQ_TOKEN
     return hipGetLastError();
   }

@@ -43,7 +43,7 @@ inline bool joins(int tile, bool gated) {
 
 // Without a workspace one split of the 256-tile
 // runs for codes, any unsplit kernel otherwise.
-inline Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool exact, bool codes, bool ws) {
+inline Plan search_plan(int64_t M, int64_t N, int64_t K, bool gated, bool exact, bool codes, bool ws) {
   const int nb = gated ? 2 : 1, e = exact ? 1 : 0;
   const int64_t kb = ceil_div(K, 128);
   Plan best{kTileKinds - 1, 1, (int)kb};
@@ -58,6 +58,9 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool exact, boo
     least = kFewLaunch + (codes ? kJoin : 0) +
             std::max((double)ceil_div(groups, 256 * here) * (kFewGroup + here * std::max(copied, issued)),
                      2.0 * groups * kb * nb / kFewWeights);
+    // codes without a gate: three 32-column tiles' conversions and more take
+    // longer than that (37 x 11008 x 4000: 27 us, 32 x 64 tiles in two splits 22)
+    if (codes && !gated && mt >= 3) least *= 1.15;
     best = {-1, 1, (int)kb};
   }
   for (int i = 0; i < kTileKinds; ++i) {
@@ -83,6 +86,20 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool exact, boo
     }
   }
   return best;
+}
+
+// search_plan with the last results of each thread kept by their arguments: a
+// call asks for the same few plans several times (its workspace's size and
+// check, its launch), a decoding loop for the same ones at every token.
+inline Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool exact, bool codes, bool ws) {
+  struct Entry { int64_t M, N, K; int how; Plan plan; };
+  static thread_local Entry kept[64] = {};
+  const int how = 16 + gated + 2 * exact + 4 * codes + 8 * ws;   // never 0
+  const uint64_t h = ((uint64_t)M * 0x9E3779B97F4A7C15ull + (uint64_t)N) * 0x9E3779B97F4A7C15ull + (uint64_t)K * 32 + how;
+  Entry& e = kept[(h * 0x9E3779B97F4A7C15ull) >> 58];
+  if (e.M != M || e.N != N || e.K != K || e.how != how)
+    e = {M, N, K, how, search_plan(M, N, K, gated, exact, codes, ws)};
+  return e.plan;
 }
 
 inline size_t plan_bytes(const Plan& p, int64_t M, int64_t N, bool gated, bool codes) {

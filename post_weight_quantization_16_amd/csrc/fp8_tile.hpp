@@ -138,6 +138,13 @@ __device__ __forceinline__ i32x4 piece16(const uint8_t* row, int64_t k, int64_t 
   return v;
 }
 
+// The source of a wide copy past a row's end, where K ends between two pieces
+// of 16 bytes: zeros.
+__device__ const uint32_t kNothing[4] __attribute__((aligned(16))) = {0, 0, 0, 0};
+__device__ __forceinline__ const uint8_t* within(const uint8_t* p, bool inside) {
+  return inside ? p : reinterpret_cast<const uint8_t*>(kNothing);
+}
+
 // ---------------------------------------------------------------- epilogues
 // Sigmoids by the hardware's exp2 and reciprocal.  What counts is the rounding
 // of the exponent: silu is within |x| + 4 units of 2^-23, gelu_tanh, whose
@@ -152,6 +159,30 @@ __device__ __forceinline__ float activate(float x, int act) {
   return over_one_plus_exp2(x, -2.30220820f * (x + 0.044715f * x * x * x));   // (1 + tanh y)/2 = 1/(1 + e^-2y)
 }
 
+// The same for many values in registers.  silu and gelu_tanh are one formula,
+// x/(1 + 2^(x·(a + b·x²))), so their values need no jumps; gelu's code stands
+// apart.  A choice at every value made the code longer than the instruction
+// cache: 4096 x 16384 x 4096 with gelu_tanh 344 us, this way 293.  (x² is limited
+// so that 0·x² stays 0.)
+struct Activation {
+  int act;
+  float a, b;
+  __device__ __forceinline__ explicit Activation(int k)
+      : act(k), a(k == GPTQ_ACT_SILU ? -1.44269504f : -2.30220820f),
+        b(k == GPTQ_ACT_SILU ? 0.f : -2.30220820f * 0.044715f) {}
+  __device__ __forceinline__ f32x4 operator()(f32x4 x) const {
+    if (__builtin_expect(act == GPTQ_ACT_GELU, 0)) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = activate(x[r], GPTQ_ACT_GELU);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        x[r] = over_one_plus_exp2(x[r], x[r] * __builtin_fmaf(fminf(x[r] * x[r], 1e38f), b, a));
+    }
+    return x;
+  }
+};
+
 // Codes of four values of a block.  1/s and the product round by 2^-24 each, so
 // a code is that of the fp32 value over its scale but within 2^-22 of a border.
 // The values and the block's largest, its scale, carry fp32's rounding already;
@@ -160,6 +191,17 @@ __device__ __forceinline__ float activate(float x, int act) {
 // fp64, which took 1487 us where this takes 1447, 2048 x 28672 x 8192 to codes).
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
   return e4m3_pack4(a * inv, b * inv, c * inv, d * inv);
+}
+
+// The same with quotients to within 2^-24 (one correction by the remainder): a
+// code differs from that of the exact quotient only next to a border.
+__device__ __forceinline__ float near_quotient(float x, float s, float inv) {
+  const float q = x * inv;
+  return __builtin_fmaf(__builtin_fmaf(-q, s, x), inv, q);
+}
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float s, float inv) {
+  return e4m3_pack4(near_quotient(a, s, inv), near_quotient(b, s, inv), near_quotient(c, s, inv),
+                    near_quotient(d, s, inv));
 }
 
 // Four neighbouring values of a row, `n` of them present.
@@ -295,14 +337,16 @@ __device__ __forceinline__ int offset_of(const GArgs& a, int e) {
 }
 template <int BM> struct Stretches {
   int per, e0, sum, below, total;
-  __device__ __forceinline__ explicit Stretches(const GArgs& a) {
+  // offsets: clamped, [E + 1]
+  __device__ __forceinline__ Stretches(const int* offsets, int E) {
     const int lane = threadIdx.x & 63;
-    per = (a.E + 63) >> 6;
+    per = (E + 63) >> 6;
     e0 = lane * per;
     sum = 0;
-    int o = offset_of(a, e0);
+    int o = offsets[min(e0, E)];
+#pragma unroll 1
     for (int j = 1; j <= per; ++j) {
-      const int p = offset_of(a, e0 + j);
+      const int p = offsets[min(e0 + j, E)];
       sum += max(p - o + BM - 1, 0) / BM;
       o = p;
     }
@@ -316,13 +360,14 @@ template <int BM> struct Stretches {
     total = __builtin_amdgcn_readlane(in, 63);
   }
   // stretch u < total
-  __device__ __forceinline__ Stretch find(const GArgs& a, int u) const {
+  __device__ __forceinline__ Stretch find(const int* offsets, int E, int u) const {
     Stretch s{0, 0, 0};
-    int left = u - below, o = offset_of(a, e0);
+    int left = u - below, o = offsets[min(e0, E)];
     const bool here = left >= 0 && left < sum;
     bool open = here;
+#pragma unroll 1
     for (int j = 1; j <= per; ++j) {
-      const int p = offset_of(a, e0 + j), n = max(p - o + BM - 1, 0) / BM;
+      const int p = offsets[min(e0 + j, E)], n = max(p - o + BM - 1, 0) / BM;
       if (open && left < n) {
         s = {e0 + j - 1, o + left * BM, min(BM, p - o - left * BM)};
         open = false;
@@ -338,7 +383,7 @@ template <int BM> struct Stretches {
   }
 };
 
-template <int BM, int BN, int WM, int WN, int NS, bool FAST, int FORM, int EPI, int DT, int ROWS = kDense>
+template <int BM, int BN, int WM, int WN, int NS, bool FAST, int FORM, int EPI, int DT>
 __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, WN, NS>::WPE)) void tile_kernel(GArgs a) {
   using T = Tile<BM, BN, WM, WN, NS>;
   constexpr bool GATED = FORM == kGated;
@@ -356,36 +401,11 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = w / (BN / WN), wn = w % (BN / WN);
-  uint32_t bm, bn, split = 0;
-  int64_t m0;
-  int mleft;
-  // ROWS: the tokens (kGather) or slots (kSorted; -1: none) of the tile's rows
-  __shared__ int row_of[ROWS == kDense ? 1 : BM];
-  if constexpr (ROWS == kDense) {
-    const uint32_t tiles = (uint32_t)a.tm * a.tn;
-    split = blockIdx.x / tiles;
-    tile_of(blockIdx.x - split * tiles, tiles, a.tm, a.tn, bm, bn);
-    m0 = (int64_t)bm * BM;
-    mleft = (int)min((int64_t)BM, a.M - m0);
-  } else {
-    const Stretches<BM> all(a);
-    const uint32_t tiles = (uint32_t)all.total * a.tn;
-    if (blockIdx.x >= tiles) return;
-    tile_of(blockIdx.x, tiles, all.total, a.tn, bm, bn);
-    const Stretch s = all.find(a, bm);
-    m0 = s.row;
-    mleft = s.rows;
-    for (int h = 0; h < NB; ++h) {
-      a.B[h] += s.expert * a.next[h];
-      a.sb[h] += (int64_t)s.expert * a.nb * a.kb;
-    }
-    if (t < BM) {
-      const int o = a.order[m0 + min(t, mleft - 1)];
-      const bool ok = o >= 0 && o < a.slots;
-      row_of[t] = ROWS == kSorted ? (ok ? o : -1) : ok ? (int)((unsigned)o / (unsigned)a.topk) : 0;
-    }
-    __syncthreads();
-  }
+  uint32_t bm, bn;
+  const uint32_t tiles = (uint32_t)a.tm * a.tn, split = blockIdx.x / tiles;
+  tile_of(blockIdx.x - split * tiles, tiles, a.tm, a.tn, bm, bn);
+  const int64_t m0 = (int64_t)bm * BM;
+  const int mleft = (int)min((int64_t)BM, a.M - m0);
   const int64_t n0 = (int64_t)bn * BC;
   const int kbeg = (int)split * a.kper, kend = min(a.kb, kbeg + a.kper);
   const int nst = kend - kbeg;
@@ -395,13 +415,13 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
   // lane l row l/8 of them, slot l%8.  Rows past the matrix copy its last
   // row (their results are never stored).
   auto seg_base = [&](int seg) -> const uint8_t* {   // wave-uniform
-    if (seg < BM / 8) return ROWS == kGather ? a.A : a.A + m0 * a.lda;
+    if (seg < BM / 8) return a.A + m0 * a.lda;
     const int half = GATED && seg >= (BM + BC) / 8;
     return a.B[half] + n0 * a.ldb[half];
   };
   auto seg_offset = [&](int seg, int l) -> int64_t {   // row and piece of lane l
     const int row = seg * 8 + (l >> 3), p16 = (((l & 7) ^ (l >> 4)) << 4) ^ ((seg & 1) << 6);
-    if (seg < BM / 8) return (int64_t)(ROWS == kGather ? row_of[row] : min(row, mleft - 1)) * a.lda + p16;
+    if (seg < BM / 8) return (int64_t)min(row, mleft - 1) * a.lda + p16;
     const int half = GATED && seg >= (BM + BC) / 8;
     return (int64_t)min(row - BM - half * BC, nleft - 1) * a.ldb[half] + p16;
   };
@@ -424,7 +444,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
 #pragma unroll
     for (int idx = w; idx < T::SCOPIES; idx += T::WAVES) {
       const float* p;
-      if (idx < BM / 8) p = a.sa + (ROWS == kGather ? (int64_t)row_of[idx * 8 + r] : m0 + min(idx * 8 + r, mleft - 1)) * a.kb;
+      if (idx < BM / 8) p = a.sa + (m0 + min(idx * 8 + r, mleft - 1)) * a.kb;
       else if (GATED) p = (r == 0 ? a.sb[0] : a.sb[NB - 1]) + n0 / 128 * a.kb;
       else p = a.sb[0] + min(n0 / 128 + min(r, 1), a.nb - 1) * a.kb;
       lds_copy4(sbase + T::SCALES + (unsigned)((g & 1) * T::SCB + idx * 256), p + k);
@@ -488,25 +508,10 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
     return {*reinterpret_cast<const i32x4*>(b + off), *reinterpret_cast<const i32x4*>(b + (off ^ 64))};
   };
 
-  float ssum[EPI == kScaled ? MI : 1];   // Σ|sa·sb| of each A piece's row
-  if constexpr (EPI == kScaled) {
-#pragma unroll
-    for (int i = 0; i < MI; ++i) ssum[i] = 0.f;
-  }
-  // a wave none of whose rows exist only copies
-  const bool idle = ROWS != kDense && wm * WM >= mleft;
   if (nst > 0) {
     copy_scales(0);
     for (int s0 = 0; s0 < NS - 1 && s0 < nst; ++s0) copy(s0, 0, T::PER);
     stage_barrier<T::PER>(min(nst - 1, NS - 2));
-  }
-  if (nst > 0 && idle) {
-    for (int st = 0; st < nst; ++st) {
-      if (st + NS - 1 < nst) copy(st + NS - 1, 0, T::PER);
-      if ((st & 7) == 0 && st + 8 < nst) copy_scales((st >> 3) + 1);
-      stage_barrier<T::PER>(min(nst - 1, st + NS - 1) - (st + 1));
-    }
-  } else if (nst > 0) {
     // The loop is software-pipelined by hand: step (i, j) multiplies A piece i
     // by B piece j and adds the product of the step before, so the matrix
     // core works while the adds run; A pieces are read one ahead, and the
@@ -537,7 +542,6 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
         sa = sn;
 #pragma unroll
         for (int q = 0; q < NB; ++q) s[q] = sa * sb[q];
-        if constexpr (EPI == kScaled) ssum[i] += fabsf(s[0]);
         if (i + 1 < MI) {
           ra = read_a(b, i + 1);
           sn = *reinterpret_cast<const float*>(sc + soff + (i + 1) * 512);
@@ -592,8 +596,8 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
         for (int r = 0; r < 4; ++r)
           acc[NI - G + g][MI - 1][r] = __builtin_fmaf(p[g][r], sp[g], acc[NI - G + g][MI - 1][r]);
     }
+    __syncthreads();   // the epilogue reuses the stage buffers
   }
-  if (nst > 0) __syncthreads();   // the epilogue reuses the stage buffers
 
   const int nl = wn * WC + 4 * (lane >> 4);   // this lane's first column in the tile
   if constexpr (EPI == kPartial) {
@@ -619,36 +623,10 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
     for (int i = 0; i < MI; ++i) {
       const int ml = wm * WM + i * 16 + l15;
       if (ml >= mleft) continue;
-      int64_t row = m0 + ml;
-      if constexpr (ROWS == kSorted) {
-        row = row_of[ml];
-        if (row < 0) continue;
-      }
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
         const int half = GATED ? j / (NI / 2) : 0, c = nl + (GATED ? j % (NI / 2) : j) * 16;
-        put4<GPTQ_F32>(P, ((int64_t)half * a.M + row) * a.N + n0 + c, nleft - c, acc[j][i]);
-      }
-    }
-    return;
-  }
-  if constexpr (EPI == kScaled) {
-    // P: fp16 [slots][N], behind it the powers of two [slots][nb]
-    _Float16* P = reinterpret_cast<_Float16*>(a.P);
-    float* F = reinterpret_cast<float*>(P + align_scaled((int64_t)a.slots * a.N));
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int ml = wm * WM + i * 16 + l15;
-      if (ml >= mleft || row_of[ml] < 0) continue;
-      const int64_t row = row_of[ml];
-      const int e = scaled_exponent(ssum[i]);
-      const float f = power_of_two(-e);
-      if (lane < 16 && (wn * WC) % 128 == 0 && nl < nleft) F[row * a.nb + (n0 + nl) / 128] = power_of_two(e);
-#pragma unroll
-      for (int j = 0; j < NI; ++j) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[j][i][r] *= f;
-        put4<GPTQ_F16>(P, row * a.N + n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+        put4<GPTQ_F32>(P, ((int64_t)half * a.M + m0 + ml) * a.N + n0 + c, nleft - c, acc[j][i]);
       }
     }
     return;
@@ -674,12 +652,11 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
       }
     }
     if (a.act >= 0) {
+      const Activation act(a.act);
 #pragma unroll
       for (int j = 0; j < NI; ++j)
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[j][i][r] = activate(acc[j][i][r], a.act);
+        for (int i = 0; i < MI; ++i) acc[j][i] = act(acc[j][i]);
     }
   }
   if constexpr (EPI == kStore && FORM == kLinear) {
@@ -743,7 +720,9 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
         a.sc[(m0 + ml) * a.nb + (BC == 128 ? bn : (uint32_t)((n0 + wn * WC) / 128))] = s;
 #pragma unroll
       for (int j = 0; j < NO; ++j) {
-        const uint32_t c = codes4(acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3], inv);
+        uint32_t c;
+        if constexpr (FORM == kLinear) c = codes4(acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3], s, inv);
+        else c = codes4(acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3], inv);
         uint8_t* o = a.codes + (m0 + ml) * a.ld_codes + n0 + nl + j * 16;
         const int n = nleft - nl - j * 16;
         if (n >= 4) {
@@ -785,7 +764,7 @@ template <int NA, bool GATED> struct Few {
   static constexpr int SMEM = WAVES * (RING > PART * 4 ? RING : PART * 4);
 };
 
-template <int NA, bool FAST, int FORM, int EPI, int ROWS = kDense>
+template <int NA, bool FAST, int FORM, int EPI>
 __global__ __launch_bounds__((Few<NA, FORM == kGated>::WAVES * 64)) void few_rows_kernel(GArgs a) {
   constexpr bool GATED = FORM == kGated;
   using F = Few<NA, GATED>;
@@ -793,30 +772,8 @@ __global__ __launch_bounds__((Few<NA, FORM == kGated>::WAVES * 64)) void few_row
   __shared__ __attribute__((aligned(1024))) char S[F::SMEM];
   const int t = threadIdx.x, lane = t & 63, l15 = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
-  int64_t n0 = (int64_t)blockIdx.x * 16, m0 = 0;
-  int mleft = (int)a.M;
-  __shared__ int row_of[ROWS == kDense ? 1 : 8 * NA];
-  if constexpr (ROWS != kDense) {
-    // column groups of a stretch side by side
-    const uint32_t u = blockIdx.x / (uint32_t)a.tn;
-    const Stretches<8 * NA> all(a);
-    if (u >= (uint32_t)all.total) return;
-    n0 = (int64_t)(blockIdx.x - u * a.tn) * 16;
-    const Stretch s = all.find(a, u);
-    m0 = s.row;
-    mleft = s.rows;
-    for (int h = 0; h < NB; ++h) {
-      a.B[h] += s.expert * a.next[h];
-      a.sb[h] += (int64_t)s.expert * a.nb * a.kb;
-    }
-    if (t < 8 * NA) {
-      const int o = a.order[m0 + min(t, mleft - 1)];
-      const bool ok = o >= 0 && o < a.slots;
-      row_of[t] = ROWS == kSorted ? (ok ? o : -1) : ok ? (int)((unsigned)o / (unsigned)a.topk) : 0;
-    }
-    __syncthreads();
-  }
-  const int nleft = (int)min((int64_t)16, a.N - n0);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int nleft = (int)min((int64_t)16, a.N - n0), mleft = (int)a.M;
   const int per = (a.kb + F::WAVES - 1) / F::WAVES;
   const int kbeg = w * per, nblk = min(per, a.kb - kbeg);   // may be 0 or less
   char* ring = S + w * F::RING;
@@ -826,16 +783,12 @@ __global__ __launch_bounds__((Few<NA, FORM == kGated>::WAVES * 64)) void few_row
   // piece l%8 to slot l%8 as in the tile kernel; rows that do not exist copy
   // the last one (their results are never stored)
   auto base = [&](int i) -> const uint8_t* {
-    return i < 2 * NB ? a.B[i / 2] + n0 * a.ldb[i / 2] : ROWS == kSorted ? a.A + m0 * a.lda : a.A;
-  };
-  auto arow = [&](int r) -> int64_t {   // row r of this workgroup, from the base
-    if constexpr (ROWS == kGather) return row_of[r < 8 * NA ? r : 8 * NA - 1];
-    return min(r, mleft - 1);
+    return i < 2 * NB ? a.B[i / 2] + n0 * a.ldb[i / 2] : a.A;
   };
   auto offset = [&](int i) -> int64_t {
     const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((i & 1) << 6);
     return i < 2 * NB ? (int64_t)min((i & 1) * 8 + (lane >> 3), nleft - 1) * a.ldb[i / 2] + p16
-                      : arow((i - 2 * NB) * 8 + (lane >> 3)) * a.lda + p16;
+                      : (int64_t)min((i - 2 * NB) * 8 + (lane >> 3), mleft - 1) * a.lda + p16;
   };
   auto dest = [&](int slot, int i) { return slot * F::SLOT + i * 1024; };
   uint32_t voff[F::PER];
@@ -848,6 +801,14 @@ __global__ __launch_bounds__((Few<NA, FORM == kGated>::WAVES * 64)) void few_row
 #pragma unroll
       for (int i = 0; i < F::PER; ++i)
         lds_copy16(rbase + (unsigned)dest(slot, i), base(i) + (int64_t)(kbeg + j) * 128, voff[i]);
+    } else if (FORM == kLinear && a.wide && a.K % 16 == 0) {
+      // K ends between two pieces (37 x 11008 x 4000 to codes 22.5 us, through registers 25.9)
+#pragma unroll
+      for (int i = 0; i < F::PER; ++i) {
+        const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((i & 1) << 6);
+        const int64_t k = (int64_t)(kbeg + j) * 128;
+        lds_copy16(rbase + (unsigned)dest(slot, i), within(base(i) + offset(i) + k, k + p16 < a.K));
+      }
     } else {
       i32x4 v[F::PER];
 #pragma unroll
@@ -865,7 +826,7 @@ __global__ __launch_bounds__((Few<NA, FORM == kGated>::WAVES * 64)) void few_row
     const int r = lane >> 3, k = min(kbeg + 8 * g + (lane & 7), a.kb - 1);
 #pragma unroll
     for (int i = 0; i < 2 * MT + 1; ++i) {
-      const float* p = i < 2 * MT ? a.sa + ((ROWS == kSorted ? m0 : 0) + arow(i * 8 + r)) * a.kb
+      const float* p = i < 2 * MT ? a.sa + (int64_t)min(i * 8 + r, mleft - 1) * a.kb
                                   : (r == 0 ? a.sb[0] : a.sb[NB - 1]) + n0 / 128 * a.kb;
       lds_copy4(rbase + (unsigned)(kFewDepth * F::SLOT + (g & 1) * F::SCB + i * 256), p + k);
     }
@@ -945,18 +906,14 @@ __global__ __launch_bounds__((Few<NA, FORM == kGated>::WAVES * 64)) void few_row
     float o = h[0];
     if constexpr (GATED) o = activate(h[0], a.act) * h[NB - 1];
     if constexpr (EPI == kPartial) {
-      if constexpr (ROWS == kSorted) {
-        if (row_of[m] >= 0) a.P[(int64_t)row_of[m] * a.N + n] = o;
-      } else {
-        a.P[(m0 + m) * a.N + n] = o;     // h itself: one partial, activated (kLinear: the sum)
-      }
+      a.P[(int64_t)m * a.N + n] = o;     // h itself: one partial, activated (kLinear: the sum)
     } else {
       if constexpr (FORM == kLinear) {
         if (a.bias) o += get1(a.bias, a.bias_dt, n);
         if (a.act >= 0) o = activate(o, a.act);
         if (a.R) o += get1(a.R, a.c_dt, m * a.ldr + n);
       }
-      put1(a.C, a.c_dt, (m0 + m) * a.ldc + n, o);
+      put1(a.C, a.c_dt, m * a.ldc + n, o);
     }
   }
 }
@@ -1030,8 +987,12 @@ __global__ __launch_bounds__(256) void join_kernel(GArgs a, int splits) {
     for (int i = 0; i < 8; ++i) u = max(u, mag_bits(h[0][i]));
     const float s = e4m3_scale((double)__builtin_bit_cast(float, row16_max_u32(u)));
     const float inv = 1.f / s;
-    store_codes8(a.codes + m * a.ld_codes + n, c, codes4(h[0][0], h[0][1], h[0][2], h[0][3], inv),
-                 codes4(h[0][4], h[0][5], h[0][6], h[0][7], inv));
+    if constexpr (FORM == kLinear || ROWS != kDense)
+      store_codes8(a.codes + m * a.ld_codes + n, c, codes4(h[0][0], h[0][1], h[0][2], h[0][3], s, inv),
+                   codes4(h[0][4], h[0][5], h[0][6], h[0][7], s, inv));
+    else
+      store_codes8(a.codes + m * a.ld_codes + n, c, codes4(h[0][0], h[0][1], h[0][2], h[0][3], inv),
+                   codes4(h[0][4], h[0][5], h[0][6], h[0][7], inv));
     if (lane == 0) a.sc[m * a.nb + blk] = s;
   } else {
     if (a.c_dt == GPTQ_F32) store8<GPTQ_F32>(static_cast<float*>(a.C) + m * a.ldc + n, c, h[0]);

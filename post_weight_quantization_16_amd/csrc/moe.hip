@@ -31,8 +31,8 @@ struct RouteArgs {
 };
 
 // ---------------------------------------------------------------- slots by expert
-// A stable counting sort of slot numbers by expert.  Block b's slots come
-// behind those of the blocks before it (their counts in hist), wave by wave;
+// A stable counting sort of slot numbers by expert.  A block's slots come
+// behind those of the rows of counts before its own in hist, wave by wave;
 // within 64 slots a lane finds the others of its expert by one ballot for each
 // bit of the expert's number, and its rank among them by their count below it.
 // Nothing depends on the order of atomics: those count, and nothing else.
@@ -43,8 +43,9 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ void sort_slots(const int32_t* ids, int i0, int i1, int E, int slots, const int32_t* hist,
-                           int blocks, int block, int32_t* offsets, int32_t* order, int* lds) {
+__device__ __forceinline__ void sort_slots(const int32_t* ids, int i0, int i1, int E, int slots,
+                                           const int32_t* hist, int rows, int row, int block, int blocks,
+                                           int32_t* offsets, int32_t* order, int* lds) {
   const int t = threadIdx.x, nt = blockDim.x, lane = t & 63, w = t >> 6, waves = nt >> 6;
   int* total = lds;
   int* first = lds + E;
@@ -58,17 +59,22 @@ __device__ __forceinline__ void sort_slots(const int32_t* ids, int i0, int i1, i
     const int e = ids[i];
     if (e >= 0 && e < E) atomicAdd(&counts[w * E + e], 1);
   }
-  if (hist) {   // all blocks' counts, and those of the blocks before this one
+  if (hist) {   // all rows of counts, and those before this block's
     const int parts = max(1, nt / E);
     for (int e0 = 0; e0 < E; e0 += nt) {
       const int part = t / E, e = e0 + (E < nt ? t - part * E : t);
       if (part >= parts || e >= E) continue;
       int all = 0, before = 0;
-#pragma unroll 8
-      for (int q = part; q < blocks; q += parts) {
-        const int h = hist[(int64_t)q * E + e];
-        all += h;
-        before += q < block ? h : 0;
+      for (int q0 = part; q0 < rows; q0 += 16 * parts) {
+        int h[16];   // sixteen loads in flight
+#pragma unroll
+        for (int i = 0; i < 16; ++i) h[i] = hist[(int64_t)min(q0 + i * parts, rows - 1) * E + e];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int q = q0 + i * parts;
+          all += q < rows ? h[i] : 0;
+          before += q < row ? h[i] : 0;
+        }
       }
       atomicAdd(&total[e], all);
       atomicAdd(&first[e], before);
@@ -140,12 +146,18 @@ __device__ __forceinline__ void sort_slots(const int32_t* ids, int i0, int i1, i
   }
 }
 
-__global__ __launch_bounds__(512) void sort_kernel(const int32_t* ids, int per, int slots, int E,
-                                                   const int32_t* hist, int blocks, int32_t* offsets,
-                                                   int32_t* order) {
+// Sixteen waves where many rows of counts are to be read (us, 256 rows of 128
+// experts: 10.1 with eight, 8.4 with sixteen; 84 rows of 256: 6.4, 7.3) and LDS
+// has room for each wave's own.
+int sort_threads(int E, int rows) { return rows > 128 && E <= 512 ? 1024 : 512; }
+// One block for `group` rows of counts, of `per` slots each.
+__global__ __launch_bounds__(1024) void sort_kernel(const int32_t* ids, int per, int slots, int E,
+                                                    const int32_t* hist, int rows, int group,
+                                                    int32_t* offsets, int32_t* order) {
   extern __shared__ int lds[];
-  const int i0 = (int)min((int64_t)blockIdx.x * per, (int64_t)slots), i1 = (int)min((int64_t)i0 + per, (int64_t)slots);
-  sort_slots(ids, i0, i1, E, slots, hist, blocks, blockIdx.x, offsets, order, lds);
+  const int row = blockIdx.x * group;
+  const int i0 = (int)min((int64_t)row * per, (int64_t)slots), i1 = (int)min(i0 + (int64_t)group * per, (int64_t)slots);
+  sort_slots(ids, i0, i1, E, slots, hist, rows, row, blockIdx.x, gridDim.x, offsets, order, lds);
 }
 
 __global__ __launch_bounds__(512) void count_kernel(const int32_t* ids, int per, int slots, int E, int32_t* hist) {
@@ -169,6 +181,27 @@ template <int CTRL> __device__ __forceinline__ float turned(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(b, b, CTRL, 0xF, 0xF, false));
 }
 template <int CTRL> __device__ __forceinline__ double turned(double x) { return dpp_d<CTRL>(x); }
+// The two values that lanes N apart hold (N = 16, 32), in both of them.
+template <int N> __device__ __forceinline__ void both(uint32_t v, uint32_t& a, uint32_t& b) {
+  const auto r = N == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                         : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  a = r[0];
+  b = r[1];
+}
+template <int N> __device__ __forceinline__ void both(float v, float& a, float& b) {
+  uint32_t x, y;
+  both<N>(__builtin_bit_cast(uint32_t, v), x, y);
+  a = __builtin_bit_cast(float, x);
+  b = __builtin_bit_cast(float, y);
+}
+template <int N> __device__ __forceinline__ void both(double v, double& a, double& b) {
+  const uint64_t q = __builtin_bit_cast(uint64_t, v);
+  uint32_t x, y, z, w;
+  both<N>((uint32_t)q, x, y);
+  both<N>((uint32_t)(q >> 32), z, w);
+  a = __builtin_bit_cast(double, (uint64_t)z << 32 | x);
+  b = __builtin_bit_cast(double, (uint64_t)w << 32 | y);
+}
 // Maximum and sum over the L lanes of a token (every lane gets them).
 template <int L, typename T> __device__ __forceinline__ T lanes_max(T v) {
   v = larger(v, turned<kRor8>(v));
@@ -176,8 +209,11 @@ template <int L, typename T> __device__ __forceinline__ T lanes_max(T v) {
   v = larger(v, turned<kRor2>(v));
   v = larger(v, turned<kRor1>(v));
   if constexpr (L == 64) {
-    v = larger(v, __shfl_xor(v, 16));
-    v = larger(v, __shfl_xor(v, 32));
+    T a, b;
+    both<16>(v, a, b);
+    v = larger(a, b);
+    both<32>(v, a, b);
+    v = larger(a, b);
   }
   return v;
 }
@@ -187,8 +223,11 @@ template <int L> __device__ __forceinline__ double lanes_sum(double v) {
   v += turned<kRor2>(v);
   v += turned<kRor1>(v);
   if constexpr (L == 64) {
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
+    double a, b;
+    both<16>(v, a, b);
+    v = a + b;
+    both<32>(v, a, b);
+    v = a + b;
   }
   return v;
 }
@@ -203,13 +242,30 @@ __device__ __forceinline__ double sigmoid(double x) { return 1.0 / (1.0 + exp(-x
 template <bool S> struct KeyOf { typedef float type; };
 template <> struct KeyOf<true> { typedef double type; };
 
+// V neighbouring logits from `at` on, those past n (0 or less: none) -inf.
+template <int DT, int V> __device__ __forceinline__ void logits_of(const void* X, int64_t at, int n, float (&x)[V]) {
+  typedef typename Elem<DT>::type T;
+  const T* p = static_cast<const T*>(X) + at;
+  if (n >= V) {
+    T v[V];
+    __builtin_memcpy(v, p, sizeof v);
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = Elem<DT>::up(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = j < n ? Elem<DT>::up(p[j]) : -__builtin_inff();
+  }
+}
+
 // L lanes a token, V neighbouring experts a lane, so that the lowest lane with
-// the largest key holds the lowest expert with it.  Sixteen lanes reduce by DPP
-// alone; 64 where 16 would hold more than 16 experts each.
+// the largest key holds the lowest expert with it.  64 lanes a token where few
+// tokens wait for the chain of one (333 tokens over 256 experts in groups: 22.4
+// us with 16 lanes, 10.0 with 64) or 16 lanes would hold more than 16 experts each;
+// 16 where the card is full, four tokens a wave (16384 over 128: 11.6 and 23.4).
 // SCORED: the choice needs p (a bias, or groups by their best two); otherwise
 // the keys are the logits, in fp32, which holds them exactly.
 // ONE: one block routes all tokens and sorts their slots too.
-constexpr int route_threads(int L, int V) { return L == 16 && V <= 8 ? 1024 : 256; }
+constexpr int route_threads(int L, int V) { return L * V <= 256 && V <= 8 ? 1024 : 256; }
 template <int L, int V, bool SCORED, bool ONE>
 __global__ __launch_bounds__(route_threads(L, V)) void route_kernel(RouteArgs a) {
   typedef typename KeyOf<SCORED>::type Key;
@@ -219,7 +275,8 @@ __global__ __launch_bounds__(route_threads(L, V)) void route_kernel(RouteArgs a)
   double* P = smem + mine * a.k;                                   // [here][k]: what was chosen
   double* rest = smem + here * a.k;
   Key* K = reinterpret_cast<Key*>(rest) + mine * a.E;              // [here][E], groups only
-  if (a.groups > 1) rest += here * a.E;
+  Key* B = reinterpret_cast<Key*>(rest + here * a.E) + 2 * t;      // [here][L][2], groups only
+  if (a.groups > 1) rest += here * (a.E + 2 * L);
   int* I = reinterpret_cast<int*>(rest) + mine * a.k;              // [here][k]
   int* hist = reinterpret_cast<int*>(rest) + here * a.k;           // [E]
   const bool count = !ONE && a.hist;
@@ -237,12 +294,11 @@ __global__ __launch_bounds__(route_threads(L, V)) void route_kernel(RouteArgs a)
     float x[V];
     bool nan = false;
     float top = none;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = l * V + j;
-      x[j] = none;
-      if (on && e < a.E) x[j] = get1(a.X, a.dt, tok * a.ld + e);
-    }
+    const int n = on ? a.E - l * V : 0;
+    const int64_t at = tok * a.ld + l * V;
+    if (a.dt == GPTQ_F32) logits_of<GPTQ_F32>(a.X, at, n, x);
+    else if (a.dt == GPTQ_BF16) logits_of<GPTQ_BF16>(a.X, at, n, x);
+    else logits_of<GPTQ_F16>(a.X, at, n, x);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       nan |= x[j] != x[j] || (soft && x[j] == __builtin_inff());
@@ -288,24 +344,35 @@ __global__ __launch_bounds__(route_threads(L, V)) void route_kernel(RouteArgs a)
         else K[e] = key[j];
       }
       wave_sync();
-      // lane g: group g, from a place of its own on, so that the lanes read different banks
+      // each group's best two by L / groups lanes, then by its own
+      const int parts = L / a.groups, g = l / parts, q = l - g * parts;
       Key one = none, two = none;
-      if (l < a.groups) {
-        int q = l % size;
-        for (int i = 0; i < size; ++i) {
-          const Key v = K[l * size + q];
+      if (g < a.groups)
+        for (int i = q; i < size; i += parts) {
+          const Key v = K[g * size + i];
           two = larger(two, v < one ? v : one);
           one = larger(one, v);
-          q = q + 1 < size ? q + 1 : 0;
+        }
+      B[0] = one;
+      B[1] = two;
+      wave_sync();
+      one = none;
+      two = none;
+      if (l < a.groups) {
+        const Key* P2 = reinterpret_cast<Key*>(smem + here * (a.k + a.E)) + 2 * (t - l + l * parts);
+        for (int i = 0; i < 2 * parts; ++i) {
+          const Key v = P2[i];
+          two = larger(two, v < one ? v : one);
+          one = larger(one, v);
         }
       }
       Key score = a.group_top == 2 && two > none ? one + two : one;
       uint32_t kept = 0;
       for (int r = 0; r < a.top_groups; ++r) {
         const Key best = lanes_max<L>(score);
-        const int g = lanes_first<L>(best > none && score == best, lane);
-        if (g < L) kept |= 1u << g;
-        if (l == g) score = none;
+        const int first = lanes_first<L>(best > none && score == best, lane);
+        if (first < L) kept |= 1u << first;
+        if (l == first) score = none;
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -364,6 +431,7 @@ __global__ __launch_bounds__(route_threads(L, V)) void route_kernel(RouteArgs a)
         id = r;
         v = __builtin_nan("");
       }
+      if constexpr (ONE) I[r] = live ? id : -1;
       if (live) {
         a.ids[tok * a.k + r] = id;
         a.weights[tok * a.k + r] = id < 0 ? 0.f : (float)v;
@@ -375,7 +443,23 @@ __global__ __launch_bounds__(route_threads(L, V)) void route_kernel(RouteArgs a)
   if constexpr (ONE) {
     __threadfence_block();
     __syncthreads();
-    sort_slots(a.ids, 0, a.T * a.k, a.E, a.T * a.k, nullptr, 1, 0, a.offsets, a.order, reinterpret_cast<int*>(smem));
+    const int slots = a.T * a.k;
+    if (slots <= 64) {   // all of them in a wave
+      const int* ids = I - mine * a.k;
+      for (int e = t; e <= a.E; e += blockDim.x) {
+        int n = 0;
+        for (int i = 0; i < slots; ++i) n += (unsigned)ids[i] < (unsigned)e;
+        a.offsets[e] = n;
+      }
+      if (t < slots) {
+        const unsigned id = (unsigned)ids[t];   // none: the largest
+        int n = 0;
+        for (int i = 0; i < slots; ++i) n += (unsigned)ids[i] < id || ((unsigned)ids[i] == id && i < t);
+        a.order[n] = (int)id < 0 ? -1 : t;
+      }
+      return;
+    }
+    sort_slots(a.ids, 0, a.T * a.k, a.E, a.T * a.k, nullptr, 1, 0, 0, 1, a.offsets, a.order, reinterpret_cast<int*>(smem));
   } else if (count) {
     __syncthreads();
     for (int e = t; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * a.E + e] = hist[e];
@@ -386,19 +470,24 @@ constexpr int kMaxBlocks = 256;   // rows of hist: every sorting block reads the
 
 // How T tokens are routed.
 struct RoutePlan { int lanes, v, threads, per, blocks; bool one; size_t lds; };
+constexpr int64_t kFewTokens = 2048;   // up to here a token gets a wave
 RoutePlan route_plan(int64_t T, int E, int k, int groups) {
   RoutePlan p;
-  p.lanes = E <= 256 ? 16 : 64;
+  const bool one_lanes = T <= 64 && E <= 128 && groups == 1;   // one block does it all
+  p.lanes = E <= 128 && T > (one_lanes ? 16 : kFewTokens) ? 16 : 64;
   p.v = 1;
   while (p.v * p.lanes < E) p.v *= 2;
-  // few tokens or many: blocks of 16 waves, so that one block does it all, or
-  // 256 of them fill the card; groups' keys leave LDS for 4
-  p.threads = route_threads(p.lanes, p.v) == 1024 && groups == 1 && (T > 4096 || T <= 64) ? 1024 : 256;
+  // blocks of 16 waves where one then does it all, or 256 of them fill the
+  // card; with 16 lanes a token, groups' keys leave LDS for 4
+  p.threads = 256;
+  if (route_threads(p.lanes, p.v) == 1024 && (groups == 1 || p.lanes == 64) &&
+      (T > kMaxBlocks * (256 / p.lanes) || (T > 256 / p.lanes && T <= 1024 / p.lanes)))
+    p.threads = 1024;
   const int here = p.threads / p.lanes;
   p.one = T <= here;
   p.per = (int)(ceil_div(ceil_div(T, kMaxBlocks), here) * here);
   p.blocks = (int)ceil_div(T, std::max(p.per, 1));
-  p.lds = (size_t)here * k * 12 + (groups > 1 ? (size_t)here * E * 8 : 0) + (size_t)E * 4;
+  p.lds = (size_t)here * k * 12 + (groups > 1 ? (size_t)here * (E + 2 * p.lanes) * 8 : 0) + (size_t)E * 4;
   if (p.one) p.lds = std::max(p.lds, (size_t)E * (2 + p.threads / 64) * 4);
   return p;
 }
@@ -407,7 +496,7 @@ template <bool SCORED, bool ONE> hipError_t launch_route(const RouteArgs& a, con
 #define GQ_ROUTE(L, V) \
   if (p.lanes == L && p.v == V) route_kernel<L, V, SCORED, ONE><<<ONE ? 1 : p.blocks, p.threads, p.lds, s>>>(a)
   GQ_ROUTE(16, 1); GQ_ROUTE(16, 2); GQ_ROUTE(16, 4); GQ_ROUTE(16, 8); GQ_ROUTE(16, 16);
-  GQ_ROUTE(64, 8); GQ_ROUTE(64, 16);
+  GQ_ROUTE(64, 1); GQ_ROUTE(64, 2); GQ_ROUTE(64, 4); GQ_ROUTE(64, 8); GQ_ROUTE(64, 16);
 #undef GQ_ROUTE
   return hipGetLastError();
 }
@@ -416,14 +505,24 @@ template <bool ONE> hipError_t launch_route(const RouteArgs& a, const RoutePlan&
   return scored ? launch_route<true, ONE>(a, p, s) : launch_route<false, ONE>(a, p, s);
 }
 
-constexpr int kSortThreads = 512, kSortAlone = 4096;   // slots that one block sorts
-size_t sort_lds(int E) { return (size_t)E * (2 + kSortThreads / 64) * 4; }
+constexpr int kSortAlone = 4096;   // slots that one block sorts
+// Each block reads all rows of counts, 256 at most: a quarter as many blocks
+// (16384 tokens, top 8 of 128: 13.3 us with one for each row, 8.4 with one for four).
+constexpr int kRowsEach = 4;
+hipError_t launch_sort(const int32_t* ids, int per, int slots, int E, const int32_t* hist, int rows,
+                       int32_t* offsets, int32_t* order, hipStream_t s) {
+  const int threads = sort_threads(E, rows);
+  const size_t lds = (size_t)E * (2 + threads / 64) * 4;
+  sort_kernel<<<(unsigned)ceil_div(rows, kRowsEach), threads, lds, s>>>(ids, per, slots, E, hist, rows, kRowsEach,
+                                                                        offsets, order);
+  return hipGetLastError();
+}
 
 }  // namespace
 
 // counts of the blocks; 256 where one block does all of it, whatever the groups
 size_t moe_ws_bytes(int64_t T, int64_t E, int64_t k) {
-  if (T <= 4 && T * k <= kSortAlone) return 256;
+  if (T <= (E <= 256 ? 16 : 4)) return 256;
   return std::max<size_t>(512, align_up((size_t)std::min<int64_t>(kMaxBlocks, ceil_div(T * k, 4)) * E * 4));
 }
 
@@ -432,15 +531,13 @@ hipError_t moe_plan_launch(const int32_t* ids, int64_t T, int k, int E, int32_t*
   const int slots = (int)(T * k);
   int32_t* hist = static_cast<int32_t*>(ws);
   if (slots <= kSortAlone) {
-    sort_kernel<<<1, kSortThreads, sort_lds(E), s>>>(ids, slots, slots, E, nullptr, 1, offsets, order);
-    return hipGetLastError();
+    return launch_sort(ids, slots, slots, E, nullptr, 1, offsets, order, s);
   }
   const int per = (int)(ceil_div(ceil_div(slots, kMaxBlocks), 512) * 512), blocks = (int)ceil_div(slots, per);
-  count_kernel<<<blocks, kSortThreads, (size_t)E * 4, s>>>(ids, per, slots, E, hist);
+  count_kernel<<<blocks, 512, (size_t)E * 4, s>>>(ids, per, slots, E, hist);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  sort_kernel<<<blocks, kSortThreads, sort_lds(E), s>>>(ids, per, slots, E, hist, blocks, offsets, order);
-  return hipGetLastError();
+  return launch_sort(ids, per, slots, E, hist, blocks, offsets, order, s);
 }
 
 hipError_t moe_route_launch(const void* X, int dt, int64_t T, int E, int64_t ld, const float* bias,
@@ -454,9 +551,7 @@ hipError_t moe_route_launch(const void* X, int dt, int64_t T, int E, int64_t ld,
   if (offsets) a.hist = static_cast<int32_t*>(ws);
   hipError_t e = launch_route<false>(a, p, s);
   if (e != hipSuccess || !offsets) return e;
-  sort_kernel<<<p.blocks, kSortThreads, sort_lds(E), s>>>(ids, p.per * k, (int)(T * k), E, a.hist, p.blocks,
-                                                         offsets, order);
-  return hipGetLastError();
+  return launch_sort(ids, p.per * k, (int)(T * k), E, a.hist, p.blocks, offsets, order, s);
 }
 
 }  // namespace gq

@@ -331,6 +331,11 @@ EXPERTS = [  # T, E, k, N, K, which experts
     (100, 4, 1, 700, 640, "one"), (130, 16, 4, 384, 520, "spread"), (200, 5, 2, 1000, 256, "spread"), (333, 128, 8, 136, 384, "few"),
     (500, 8, 2, 513, 300, "twice"), (700, 8, 2, 1280, 256, "gaps"), (1000, 2, 1, 640, 384, "spread"), (1500, 16, 4, 256, 300, "spread"),
     (300, 1024, 8, 64, 128, "spread"), (1024, 3, 3, 385, 129, "spread"), (40, 300, 16, 40, 200, "few"),
+    # few columns and tokens, K cut between two pieces of 16; blocks that end in K = 1040 and 2704
+    (2, 64, 8, 300, 400, "spread"), (1, 16, 1, 100, 1040, "spread"), (8, 32, 4, 60, 144, "gaps"), (30, 6, 2, 200, 2704, "spread"),
+    # many tiles for each workgroup, products with and without a stream, short ones
+    (300, 16, 1, 4500, 520, "spread"), (250, 12, 1, 5600, 300, "gaps"), (900, 8, 1, 7000, 400, "spread"), (900, 8, 1, 7000, 130, "spread"),
+    (2000, 4, 1, 8500, 700, "spread"), (1300, 3, 1, 13000, 200, "spread"), (300, 4, 2, 200, 2704, "spread"), (700, 2, 1, 300, 2700, "spread"),
 ]
 
 
