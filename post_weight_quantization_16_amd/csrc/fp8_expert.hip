@@ -927,7 +927,9 @@ size_t fp8_expert_gated_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t N) {
 }
 size_t fp8_expert_gemm_ws_bytes(int64_t T, int64_t k, int64_t N) {
   if (T <= kTokens && T * k <= kTokenSlots) return 256;
-  return std::max<size_t>(512, align_up((size_t)(T * k) * N * 4));
+  // fp32 terms, or fp16 ones with a power of two for each block of columns
+  const int64_t n = T * k * N;
+  return std::max<size_t>(512, align_up((size_t)std::max(n * 4, align_scaled(n) * 2 + T * k * ceil_div(N, 128) * 4)));
 }
 
 hipError_t fp8_expert_gated_launch(const uint8_t* A, const float* sa, int64_t T, int64_t K, int64_t lda,

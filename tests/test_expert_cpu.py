@@ -135,6 +135,8 @@ def test_expert_product_refusals():
     assert back(T=0, H=None, C=None, ws=None, wsb=0) == n.OK
     for which in (n.WS_MOE, n.WS_EXPERT_GATED, n.WS_EXPERT_GEMM):
         assert size(which, -1, 2, 8, 64, 256) == 0 and size(which, 4, 9, 8, 64, 256) == 0 and size(which, 4, 2, 0, 64, 256) == 0
+    for T, N in [(1000, 1), (999, 2), (70, 3), (500, 130), (40, 4096)]:    # fp16 terms and their powers of two, or fp32 terms
+        assert size(n.WS_EXPERT_GEMM, T, 2, 8, N, 256) >= max(8 * T * N, 2 * -(-2 * T * N // 8) * 8 + 8 * T * -(-N // 128))
     assert size(n.WS_EXPERT_GEMM, 4, 2, 8, 0, 256) == 0 and size(n.WS_EXPERT_GATED, 4, 2, 8, 64, 0) == 0 and size(99, 4, 2, 8, 64, 256) == 0
 
 

@@ -335,6 +335,7 @@ EXPERTS = [  # T, E, k, N, K, which experts
     (2, 64, 8, 300, 400, "spread"), (1, 16, 1, 100, 1040, "spread"), (8, 32, 4, 60, 144, "gaps"), (30, 6, 2, 200, 2704, "spread"),
     # many tiles for each workgroup, products with and without a stream, short ones
     (300, 16, 1, 4500, 520, "spread"), (250, 12, 1, 5600, 300, "gaps"), (900, 8, 1, 7000, 400, "spread"), (900, 8, 1, 7000, 130, "spread"),
+    (1000, 8, 2, 1, 200, "spread"), (300, 4, 2, 3, 130, "gaps"),      # terms beside as many bytes of powers of two
     (2000, 4, 1, 8500, 700, "spread"), (1300, 3, 1, 13000, 200, "spread"), (300, 4, 2, 200, 2704, "spread"), (700, 2, 1, 300, 2700, "spread"),
 ]
 
