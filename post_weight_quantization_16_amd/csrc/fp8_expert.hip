@@ -849,8 +849,10 @@ void finish_args(GArgs& a) {
   a.kb = (int)ceil_div(a.K, 128);
   a.kper = a.kb;
 }
-bool wide_rows(const uint8_t* q, int64_t rows, int64_t ld, int64_t most) {
-  return (uintptr_t)q % 16 == 0 && (rows == 1 || (ld % 16 == 0 && ld * std::min(rows, most) < ((int64_t)1 << 31)));
+// Whether copies of 16 bytes can take the rows of an operand, `span` of which the
+// 32-bit offsets from one base reach over.
+bool wide_rows(const uint8_t* q, int64_t ld, int64_t span) {
+  return (uintptr_t)q % 16 == 0 && ld % 16 == 0 && ld <= ((int64_t)1 << 31) / span;
 }
 
 // Rows of an expert, on average over those that can have any.
@@ -938,6 +940,9 @@ hipError_t fp8_expert_gated_launch(const uint8_t* A, const float* sa, int64_t T,
                                    const uint8_t* U, const float* su, int64_t ldu, int64_t next_u,
                                    int64_t N, int act, void* C, int c_dt, int64_t ldc, uint8_t* codes,
                                    int64_t ld_codes, float* sc, void* ws, hipStream_t s) {
+  // a row alone has no next one
+  if (T == 1) lda = 0;
+  if (N == 1) ldg = ldu = 0;
   GArgs a{};
   a.A = A; a.sa = sa; a.M = T * k; a.K = K; a.lda = lda;
   a.B[0] = G; a.sb[0] = sg; a.ldb[0] = ldg; a.next[0] = next_g;
@@ -947,8 +952,8 @@ hipError_t fp8_expert_gated_launch(const uint8_t* A, const float* sa, int64_t T,
   a.codes = codes; a.ld_codes = ld_codes; a.sc = sc;
   a.offsets = offsets; a.order = order; a.E = E; a.topk = k; a.slots = (int)(T * k);
   finish_args(a);
-  a.wide = wide_rows(A, T, lda, T) && wide_rows(G, 2, ldg, 256) && wide_rows(U, 2, ldu, 256) &&
-           next_g % 16 == 0 && next_u % 16 == 0;
+  a.wide = wide_rows(A, lda, T) && wide_rows(G, ldg, 256) && wide_rows(U, ldu, 256) && next_g % 16 == 0 &&
+           next_u % 16 == 0;
   a.P = static_cast<float*>(ws);
   if (codes) return run_gated<kCodes, GPTQ_F32>(a, s);
   if (c_dt == GPTQ_F32) return run_gated<kStore, GPTQ_F32>(a, s);
@@ -961,13 +966,15 @@ hipError_t fp8_expert_gemm_launch(const uint8_t* A, const float* sa, int64_t T, 
                                   const int32_t* order, int E, const uint8_t* B, const float* sb,
                                   int64_t ldb, int64_t next, int64_t N, const void* R, int64_t ldr,
                                   void* C, int c_dt, int64_t ldc, void* ws, hipStream_t s) {
+  if (T * k == 1) lda = 0;
+  if (N == 1) ldb = 0;
   GArgs a{};
   a.A = A; a.sa = sa; a.M = T * k; a.K = K; a.lda = lda;
   a.B[0] = B; a.sb[0] = sb; a.ldb[0] = ldb; a.next[0] = next;
   a.N = N; a.P = static_cast<float*>(ws);
   a.offsets = offsets; a.order = order; a.E = E; a.topk = k; a.slots = (int)(T * k);
   finish_args(a);
-  a.wide = wide_rows(A, 2, lda, 256) && wide_rows(B, 2, ldb, 256) && next % 16 == 0;
+  a.wide = wide_rows(A, lda, 256) && wide_rows(B, ldb, 256) && next % 16 == 0;
   hipError_t e;
   a.R = R; a.ldr = ldr; a.C = C; a.c_dt = c_dt; a.ldc = ldc;
   if (T <= kTokens && T * k <= kTokenSlots) {

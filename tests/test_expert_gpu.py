@@ -434,6 +434,33 @@ def test_experts_take_any_stride_and_leave_the_rest(T, E, k, N, K):
         assert _same(gq().fp8_expert_gemm(hh, r, dd, out=wide[:, :N]), wy) and torch.all(wide[:, N:] == 7)
 
 
+@pytest.mark.parametrize("T", [2, 40, 300])
+def test_experts_take_rows_far_apart(T):
+    """Offsets within a tile's rows past 32 bits: weights as [N, E, K], and
+    activations that are columns of something wide."""
+    torch = torch_mod()
+    F, X, E4 = gq().Fp8Matrix, gq().Fp8Experts, _t("fp8")
+    E, k, N, K, ld = 3, 2, 140, 260, (1 << 25) + 16
+    ids, w = _choice(T, E, k, 1)
+    r = gq().moe_plan(ids, w, E)
+    a, g_, u = _matrix(T, K, 1, 1), _experts(E, N, K, 2), _experts(E, N, K, 3)
+    h, d = _matrix(T * k, K, 1, 4), _experts(E, N, K, 5)
+    want, wy = gq().fp8_expert_gated_gemm(a, r, g_, u), gq().fp8_expert_gemm(h, r, d)
+    big = torch.empty((max(N, 2 * T) - 1) * ld + (1 << 20), dtype=torch.uint8, device="cuda")
+
+    def far(m, at):
+        shape = tuple(m.codes.shape)
+        v = torch.as_strided(big, shape, ((4096,) if len(shape) == 3 else ()) + (ld, 1), at)
+        v.copy_(m.codes.view(torch.uint8))
+        return X(v.view(E4), m.scales) if len(shape) == 3 else F(v.view(E4), m.scales, 1)
+
+    aa, hh, gg, uu, dd = far(a, 0), far(h, 1 << 15), far(g_, 1 << 16), far(u, 1 << 17), far(d, 1 << 18)
+    assert gg.codes[0, N - 1].data_ptr() - gg.codes.data_ptr() > 1 << 32
+    assert _same(gq().fp8_expert_gated_gemm(aa, r, gg, uu), want)
+    assert _same(gq().fp8_expert_gated_gemm(aa, r, g_, u), want) and _same(gq().fp8_expert_gated_gemm(a, r, gg, uu), want)
+    assert _same(gq().fp8_expert_gemm(hh, r, dd), wy) and _same(gq().fp8_expert_gemm(h, r, dd), wy)
+
+
 @pytest.mark.parametrize("T", [3, 40, 300])
 def test_experts_keep_what_is_not_finite_with_its_tokens(T):
     """A NaN token, a NaN expert and a NaN weight reach the outputs that they
