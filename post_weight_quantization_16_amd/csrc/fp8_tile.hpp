@@ -317,9 +317,11 @@ enum { kStore = 0, kPartial = 1, kCodes = 2, kScaled = 3 };
 // The power of two for kScaled, from s = Σ|sa·sb| over the row's blocks: codes
 // are 448 at most, so a sum is below s·128·448² < s·2^24.63 and, times 2^-(11 +
 // exponent of s), below 2^14.63: fp16 holds it.  Usual sums are 2^9 to 2^12
-// smaller, still 2^15 above the last normal number of fp16.
+// smaller, still 2^15 above the last normal number of fp16.  The limits keep the
+// power an fp32 number; beyond the upper one fp32's own largest sum, times
+// 2^-124, is 2^4.
 __device__ __forceinline__ int scaled_exponent(float s) {
-  return min(max((int)((__builtin_bit_cast(uint32_t, s) >> 23) & 0xFF) - 127, -100), 100) + 11;
+  return min(max((int)((__builtin_bit_cast(uint32_t, s) >> 23) & 0xFF) - 127, -126), 113) + 11;
 }
 __device__ __forceinline__ float power_of_two(int e) {
   return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);

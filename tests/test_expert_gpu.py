@@ -491,6 +491,21 @@ def test_experts_keep_what_is_not_finite_with_its_tokens(T):
     assert torch.equal(torch.isnan(y), bad) and torch.equal(y[~bad], wy[~bad])
 
 
+def test_expert_sums_near_the_ends_of_fp32():
+    """Terms for bf16 sums keep fp32's range: products just below 2^128, and
+    scales whose products are tiny."""
+    torch = torch_mod()
+    T, E, k, N, K = 40, 2, 1, 130, 256
+    ids, w = torch.arange(T, device="cuda").remainder(E).int()[:, None], torch.ones(T, k, device="cuda")
+    r = gq().moe_plan(ids, w, E)
+    for p, code in [(123, 24.0), (110, 3.0), (100, 1.0), (0, 1.0), (-100, 1.0), (-118, 2.0)]:
+        h = gq().Fp8Matrix(torch.zeros(T, K, device="cuda").to(_t("fp8")), torch.full((T, 2), 2.0 ** (p - p // 2), device="cuda"), 1)
+        h.codes[:, 5] = 1.0
+        d = gq().Fp8Experts(torch.full((E, N, K), code, device="cuda").to(_t("fp8")), torch.full((E, 2, 2), 2.0 ** (p // 2), device="cuda"))
+        y = gq().fp8_expert_gemm(h, r, d)
+        assert torch.all(y.double() == code * 2.0 ** p), p
+
+
 def test_experts_with_all_tokens_padding():
     torch = torch_mod()
     for T in (4, 90):
