@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* P, int64_t nb,
   for (int i = 0; i < 8; ++i) y[i] = 0.f;
   // four slots' loads in flight
   for (int j0 = 0; j0 < k; j0 += 4) {
-    float v[4][8], w[4];
+    float v[4][8], w[4], f[4];
     bool on[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* P, int64_t nb,
       if (!on[u]) continue;
       if constexpr (SCALED) {
         load8<GPTQ_F16>(H + s * N + n, c, v[u]);
-        w[u] *= F[s * nb + n / 128];
+        f[u] = F[s * nb + n / 128];
       } else {
         load8<GPTQ_F32>(static_cast<const float*>(P) + s * N + n, c, v[u]);
       }
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* P, int64_t nb,
     for (int u = 0; u < 4; ++u)
       if (on[u]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(w[u], v[u][i], y[i]);
+        for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(w[u], SCALED ? v[u][i] * f[u] : v[u][i], y[i]);
       }
   }
   if (R) {
