@@ -906,11 +906,18 @@ template <int EPI, int DT> hipError_t run_gated(GArgs& a, hipStream_t s) {
 //   128 x 128   35.7 / 110    42.6 / 142    68 / 185      189 / 344
 //   128 x 256   33.4 / 98     40.8 / 125    63 / 172      177 / 322
 //   256 x 256   39.6 / 121    45.3 / 151    87 / 200      167 / 367
-// (exact 256-row tiles have no registers left).  Bound: at few rows the weights'
-// bytes, at many the stores of the terms, which a tile's last stages wait for.
+// (exact 256-row tiles have no registers left).  Where a tile of 128 rows for
+// each expert leaves three CUs in four idle, small tiles win for as long as those
+// would be one to an expert (16 experts of 1024 x 4096, 64 tiles, 64 / 96 / 128
+// rows: 32.5 / 33.2 / 48.4 against 44.9 / 47.0 / 47.6; with twice the columns
+// 54.4 / 63.6 against 48.5 / 51.4).  Bound: at few rows the weights' bytes, at
+// many the stores of the terms, which a tile's last stages wait for (a tile's
+// sums kept in registers and stored a piece at a time under the next one's
+// stages: 170.8 at 512 rows, 188 at 32 of the second, no gain).
 template <bool FAST, int EPI> hipError_t run_sorted(GArgs& a, hipStream_t s) {
   const double r = rows_each(a);
-  if (r < 48) return launch_tiles<32, 128, 32, 32, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, true>(a, s);
+  const bool few = r <= 112 && std::min(a.slots, a.E) * ceil_div(a.N, 256) <= 64;
+  if (r < 48 || few) return launch_tiles<32, 128, 32, 32, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, true>(a, s);
   if (!FAST || r < 300) {
     if (a.kb > 20) return launch_tiles<128, 256, 64, 64, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, false>(a, s);
     return launch_tiles<128, 256, 64, 64, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, true>(a, s);
