@@ -66,6 +66,12 @@ __device__ __forceinline__ void lds_copy4(unsigned lds, const void* a) {
                :: "s"(lds), "v"(a) : "m0", "memory");
 }
 
+// What a wave's lanes wrote to LDS is read by its other lanes behind this.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 inline size_t align_up(size_t x, size_t a = 256) { return (x + a - 1) / a * a; }
 
 // ---------------------------------------------------------------- fp32 GEMM

@@ -721,25 +721,45 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Stream<BM, BN, WM,
         // kScaled: P is fp16 [slots][N], behind it the powers of two [slots][nb]
         _Float16* P = reinterpret_cast<_Float16*>(a.P);
         float* F = reinterpret_cast<float*>(P + align_scaled((int64_t)a.slots * a.N));
+        // kPartial: sixteen rows at a time go through LDS, so that neighbouring
+        // lanes store neighbouring bytes: the part of the last stage's place in the
+        // ring that this wave itself fills next; nobody reads it any more.  (64
+        // experts of 2048 x 1024, 512 rows: 235.6 -> 201.6 us; for kScaled, 128 bytes
+        // of a row to a wave, a swap of lanes was better: 166.9 -> 153.8, with LDS 161.7.)
+        constexpr int U = WN / 4, PIECE = 16 * U * 16, TURNS = 2 * PIECE <= T::PER * 1024 ? 2 : 1;
+        static_assert(PIECE <= T::PER * 1024 && T::SEGS % T::WAVES == 0, "place for a piece of sums");
+        char* mine = S + ((ring + nst + NS - 1) % NS) * T::SB + w * T::PER * 1024;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-          const int ml = wm * WM + i * 16 + l15;
-          const int64_t row = slots_[tab][ml];
-          if (ml >= cur.mleft || row < 0 || row >= a.slots) continue;
           if constexpr (EPI == kScaled) {
+            const int ml = wm * WM + i * 16 + l15;
+            const int64_t row = slots_[tab][ml];
+            const bool there = ml < cur.mleft && row >= 0 && row < a.slots;
             const int e = scaled_exponent(ssum[i]);
             const float f = power_of_two(-e);
-            if (lane < 16 && (wn * WC) % 128 == 0 && nl < nleft) F[row * a.nb + (cur.n0 + nl) / 128] = power_of_two(e);
-#pragma unroll
-            for (int j = 0; j < NI; ++j) {
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[j][i][r] *= f;
-              put4<GPTQ_F16>(P, row * a.N + cur.n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
-            }
-          } else {
+            if (there && lane < 16 && (wn * WC) % 128 == 0 && nl < nleft)
+              F[row * a.nb + (cur.n0 + nl) / 128] = power_of_two(e);
 #pragma unroll
             for (int j = 0; j < NI; ++j)
-              put4<GPTQ_F32>(a.P, row * a.N + cur.n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[j][i][r] *= f;
+            put_row<GPTQ_F16, NI>(P, row * a.N + cur.n0 + wn * WC, there ? nleft - wn * WC : 0, acc, i, l);
+          } else {
+            char* buf = mine + i % TURNS * PIECE;
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+              *reinterpret_cast<f32x4*>(buf + (l15 * U + ((4 * j + (l >> 4)) ^ (l15 & (U - 1)))) * 16) = acc[j][i];
+            wave_sync();
+#pragma unroll
+            for (int q = 0; q < U / 4; ++q) {
+              const int r = q * (64 / U) + l / U, u = l % U, ml = wm * WM + i * 16 + r;
+              const f32x4 x = *reinterpret_cast<const f32x4*>(buf + (r * U + (u ^ (r & (U - 1)))) * 16);
+              const int64_t row = slots_[tab][ml];
+              const int n = wn * WC + u * 4;
+              if (ml < cur.mleft && row >= 0 && row < a.slots)
+                put4<GPTQ_F32>(a.P, row * a.N + cur.n0 + n, nleft - n, x);
+            }
+            wave_sync();
           }
         }
       } else {
@@ -756,10 +776,8 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Stream<BM, BN, WM,
 #pragma unroll
           for (int i = 0; i < MI; ++i) {
             const int ml = wm * WM + i * 16 + l15;
-            if (ml >= cur.mleft) continue;
-#pragma unroll
-            for (int j = 0; j < NO; ++j)
-              put4<DT>(a.C, ((int64_t)cur.m0 + ml) * a.ldc + cur.n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+            put_row<DT, NO>(a.C, ((int64_t)cur.m0 + ml) * a.ldc + cur.n0 + wn * WC,
+                            ml < cur.mleft ? nleft - wn * WC : 0, acc, i, l);
           }
         }
       }
@@ -898,7 +916,8 @@ template <int EPI, int DT> hipError_t run_gated(GArgs& a, hipStream_t s) {
   return launch_tiles<128, 256, 64, 64, 2, FAST, kGated, EPI, DT, kGather>(a, s);
 }
 // Back, to bf16 with the sum over the slots (streams; us; 64 experts of 2048 x
-// 1024, top 8 / 256 of 4096 x 512, top 8):
+// 1024, top 8 / 256 of 4096 x 512, top 8; before sums were stored 64 bytes of a row
+// at a time, which took 3 to 9 % off from 64 rows on):
 //   rows        8 / 2         32 / 8        128 / 32      512 / 128
 //   16 x 128    34.6 / 97     48.6 / 124    122 / 204     403 / 608
 //   32 x 128    32.1 / 99     38.0 / 125    86 / 177      276 / 437
@@ -910,10 +929,13 @@ template <int EPI, int DT> hipError_t run_gated(GArgs& a, hipStream_t s) {
 // each expert leaves three CUs in four idle, small tiles win for as long as those
 // would be one to an expert (16 experts of 1024 x 4096, 64 tiles, 64 / 96 / 128
 // rows: 32.5 / 33.2 / 48.4 against 44.9 / 47.0 / 47.6; with twice the columns
-// 54.4 / 63.6 against 48.5 / 51.4).  Bound: at few rows the weights' bytes, at
-// many the stores of the terms, which a tile's last stages wait for (a tile's
-// sums kept in registers and stored a piece at a time under the next one's
-// stages: 170.8 at 512 rows, 188 at 32 of the second, no gain).
+// 54.4 / 63.6 against 48.5 / 51.4).  Bound: at few rows the weights' bytes; at many
+// (64 experts of 512 rows) 2.2 us a stage of a tile, as in a plain product of this
+// size, and 9 us a tile for its stores, of 26, in five rounds of tiles where whole
+// ones would make four.  Two ways to keep the next tile's stages from waiting for
+// stores gained nothing: sums held in registers and stored a piece at a time under
+// them (188 us in place of 184, 128 x 256), the copies of one stage more ahead of
+// the stores (159.0 in place of 157.1).
 template <bool FAST, int EPI> hipError_t run_sorted(GArgs& a, hipStream_t s) {
   const double r = rows_each(a);
   const bool few = r <= 112 && std::min(a.slots, a.E) * ceil_div(a.N, 256) <= 64;

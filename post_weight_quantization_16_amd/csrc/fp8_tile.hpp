@@ -219,6 +219,89 @@ template <int DT> __device__ __forceinline__ void put4(void* C, int64_t at, int 
       if (i < n) p[i] = v[i];
   }
 }
+// The same for two tiles that are 16 columns apart, of a 16-bit type: the odd
+// quarters of the wave change their columns of the first for the even ones' of the
+// second, so that a lane stores eight neighbouring columns (the first of them
+// eight_at(lane) from the first tile's own first) and the wave 64 bytes of a row in
+// place of 32: stores into many rows cost by their number (products to bf16, 8192 x
+// 8192 x 1024: 96.4 -> 82.4 us, 4096 x 16384 x 4096: 262.5 -> 248.4).  All lanes take
+// part; n counts from the lane's first column, none for a row that does not exist.
+// One wide store, written as such: as eight elements the compiler takes it apart.
+__device__ __forceinline__ int eight_at(int lane) { return 16 * (lane >> 4 & 1) + 8 * (lane >> 5); }
+template <int DT>
+__device__ __forceinline__ void put8(void* C, int64_t at, int n, const f32x4& x, const f32x4& y) {
+  typedef typename Elem<DT>::type T;
+  T v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = Elem<DT>::down(x[i]);
+    v[4 + i] = Elem<DT>::down(y[i]);
+  }
+  unsigned u[4];
+  __builtin_memcpy(u, v, sizeof u);
+  const auto lo = __builtin_amdgcn_permlane16_swap(u[0], u[2], false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(u[1], u[3], false, false);
+  const i32x4 w = {(int)lo[0], (int)hi[0], (int)lo[1], (int)hi[1]};
+  T* p = static_cast<T*>(C) + at;
+  if (n >= 8) {
+    __builtin_memcpy(p, &w, sizeof w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint16_t h = (uint16_t)((unsigned)w[i / 2] >> (16 * (i & 1)));
+      if (i < n) __builtin_memcpy(p + i, &h, sizeof h);
+    }
+  }
+}
+// The way back: eight neighbouring columns of a lane, those past n zeros, added to
+// its columns of the two tiles.
+template <int DT> __device__ __forceinline__ i32x4 get8_of(const void* p, int64_t at, int n) {
+  typedef typename Elem<DT>::type T;
+  const T* q = static_cast<const T*>(p) + at;
+  i32x4 w = {0, 0, 0, 0};
+  if (n >= 8) {
+    __builtin_memcpy(&w, q, sizeof w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint16_t h = 0;
+      if (i < n) __builtin_memcpy(&h, q + i, sizeof h);
+      w[i / 2] |= (int)((unsigned)h << (16 * (i & 1)));
+    }
+  }
+  return w;
+}
+template <int DT> __device__ __forceinline__ void add8(const i32x4& w, f32x4& x, f32x4& y) {
+  typedef typename Elem<DT>::type T;
+  const auto lo = __builtin_amdgcn_permlane16_swap((unsigned)w[0], (unsigned)w[2], false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap((unsigned)w[1], (unsigned)w[3], false, false);
+  const unsigned u[4] = {lo[0], hi[0], lo[1], hi[1]};
+  T v[8];
+  __builtin_memcpy(v, u, sizeof v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] += Elem<DT>::up(v[i]);
+    y[i] += Elem<DT>::up(v[4 + i]);
+  }
+}
+// Piece i of the rows of a wave's sums, NO tiles of columns, n of them present; at:
+// of the lane's row, the wave's first column.
+template <int DT, int NO, int NI, int MI>
+__device__ __forceinline__ void put_row(void* C, int64_t at, int n, const f32x4 (&acc)[NI][MI], int i, int lane) {
+  if constexpr (DT != GPTQ_F32 && NO % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < NO; j += 2) {
+      const int c = j * 16 + eight_at(lane);
+      put8<DT>(C, at + c, n - c, acc[j][i], acc[j + 1][i]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NO; ++j) {
+      const int c = j * 16 + 4 * (lane >> 4);
+      put4<DT>(C, at + c, n - c, acc[j][i]);
+    }
+  }
+}
 // Four neighbouring elements of type dt, widened; those past n are zeros.
 template <int DT> __device__ __forceinline__ f32x4 get4_of(const void* p, int64_t at, int n) {
   typedef typename Elem<DT>::type T;
@@ -662,33 +745,58 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Tile<BM, BN, WM, W
     }
   }
   if constexpr (EPI == kStore && FORM == kLinear) {
-    // residuals of a row together, so that their loads are in flight at once
+    // residuals of as many rows together as 32 registers hold: who waits for a load
+    // waits for the stores before it too (8192 x 8192 x 1024, bf16, gelu: one piece
+    // of rows at a time 213 us, four 190, all eight, which spills, 216)
+    constexpr bool PAIRS = DT != GPTQ_F32 && NO % 2 == 0;
+    constexpr int CH = PAIRS ? (MI > 4 ? 4 : MI) : (MI * NI > 8 ? 8 / NI : MI);
+    static_assert(MI % CH == 0, "chunks of rows");
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int ml = wm * WM + i * 16 + l15;
-      if (ml >= mleft) continue;
+    for (int i0 = 0; i0 < MI; i0 += CH) {
       if (a.R) {
-        f32x4 x[NI];
+        if constexpr (PAIRS) {
+          i32x4 x[CH][NO / 2];
 #pragma unroll
-        for (int j = 0; j < NI; ++j)
-          x[j] = get4_of<DT>(a.R, (m0 + ml) * a.ldr + n0 + nl + j * 16, nleft - nl - j * 16);
+          for (int i = 0; i < CH; ++i) {
+            const int ml = wm * WM + (i0 + i) * 16 + l15;
 #pragma unroll
-        for (int j = 0; j < NI; ++j)
+            for (int j = 0; j < NO; j += 2) {
+              const int n = wn * WC + j * 16 + eight_at(lane);
+              x[i][j / 2] = get8_of<DT>(a.R, (m0 + ml) * a.ldr + n0 + n, ml < mleft ? nleft - n : 0);
+            }
+          }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[j][i][r] += x[j][r];
+          for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int j = 0; j < NO; j += 2) add8<DT>(x[i][j / 2], acc[j][i0 + i], acc[j + 1][i0 + i]);
+        } else {
+          f32x4 x[CH][NI];
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int ml = wm * WM + (i0 + i) * 16 + l15;
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+              x[i][j] = get4_of<DT>(a.R, (m0 + ml) * a.ldr + n0 + nl + j * 16, ml < mleft ? nleft - nl - j * 16 : 0);
+          }
+#pragma unroll
+          for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[j][i0 + i][r] += x[i][j][r];
+        }
       }
 #pragma unroll
-      for (int j = 0; j < NI; ++j)
-        put4<DT>(a.C, (m0 + ml) * a.ldc + n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+      for (int i = i0; i < i0 + CH; ++i) {
+        const int ml = wm * WM + i * 16 + l15;
+        put_row<DT, NO>(a.C, (m0 + ml) * a.ldc + n0 + wn * WC, ml < mleft ? nleft - wn * WC : 0, acc, i, lane);
+      }
     }
   } else if constexpr (EPI == kStore) {
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       const int ml = wm * WM + i * 16 + l15;
-      if (ml >= mleft) continue;
-#pragma unroll
-      for (int j = 0; j < NO; ++j)
-        put4<DT>(a.C, (m0 + ml) * a.ldc + n0 + nl + j * 16, nleft - nl - j * 16, acc[j][i]);
+      put_row<DT, NO>(a.C, (m0 + ml) * a.ldc + n0 + wn * WC, ml < mleft ? nleft - wn * WC : 0, acc, i, lane);
     }
   } else {
     // the tile is one or two blocks of 128 columns wide, a wave within one

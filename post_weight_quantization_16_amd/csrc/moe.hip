@@ -37,12 +37,6 @@ struct RouteArgs {
 // bit of the expert's number, and its rank among them by their count below it.
 // Nothing depends on the order of atomics: those count, and nothing else.
 // LDS: total [E], first [E], counts [waves][E].
-// What a wave's lanes wrote is read by its other lanes behind this.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 __device__ __forceinline__ void sort_slots(const int32_t* ids, int i0, int i1, int E, int slots,
                                            const int32_t* hist, int rows, int row, int block, int blocks,
                                            int32_t* offsets, int32_t* order, int* lds) {
