@@ -277,6 +277,24 @@ def test_linear_in_place_strides_and_what_lies_behind(M, N, K):
     assert gq().fp8_linear(none, b, bias).shape == (0, N)
 
 
+@pytest.mark.parametrize("c", ["bf16", "f16", "f32"])
+def test_linear_adds_a_residual_to_the_largest_tiles(c):
+    """Many tiles of 256 rows, the last ones cut in both directions, with a
+    residual from elsewhere and from the place of the result."""
+    torch = torch_mod()
+    M, N, K = 2311, 8197, 140
+    a, b = _matrix(M, K, 1, 1), _matrix(N, K, 128, 2, 0.05)
+    res = _randn(M, N, seed=4, std=2.0).to(_t(c)).cuda()
+    ref, bound = moe.linear(_values(a), _values(b), None, None, _np(res))
+    got = gq().fp8_linear(a, b, residual=res, out_dtype=_t(c))
+    _check(got, ref, bound(c != "f32"), c, f"LINEAR {M}x{N}x{K} {c}")
+    wide = torch.full((M, N + 2), 7.0, dtype=_t(c), device="cuda")
+    wide[:, 1:N + 1] = res
+    same = wide[:, 1:N + 1]
+    assert gq().fp8_linear(a, b, residual=same, out=same) is same
+    assert _same(same, got) and torch.all(wide[:, 0] == 7) and torch.all(wide[:, N + 1] == 7)
+
+
 @pytest.mark.parametrize("M", [5, 70, 300])
 def test_linear_keeps_what_is_not_finite_in_its_place(M):
     torch = torch_mod()
