@@ -11,7 +11,7 @@
 // one pass adds a token's slots, with their weights, in the order of j.  For
 // bf16 results these sums are rounded to fp16 on their way (kScaled): 2^-11 of
 // each term, an eighth of what the result's own rounding may lose, for half the
-// bytes (4096 tokens, top 8, 2048 columns: 227 -> 170 us).
+// bytes (4096 tokens, top 8, 2048 columns: 200 -> 153 us).
 #include <cmath>
 
 #include "fp8_tile.hpp"
