@@ -612,8 +612,13 @@ int gptq_fp8_expert_gated_gemm(const uint8_t* A, const float* a_scales, int64_t 
  *   y[t] = Σ_j weights[t,j]·(h[i(t,j)]·D_eᵀ) + residual[t], one rounding,
  * i(t,j) the sorted position of slot t·top_k + j; slots without an expert add
  * nothing.  Products as in gptq_fp8_gemm (exact with fp32 sums for GPTQ_F32);
- * the sum over j is fp32.  For GPTQ_BF16 its terms h·D_eᵀ may be rounded to 11
- * bits first, an eighth of what C's own rounding may lose.
+ * the sum over j is fp32.  For GPTQ_BF16, with more than 16 tokens or 128 slots,
+ * each term h·D_eᵀ is rounded to fp16 first, times a power of two for each row
+ * of up to 64 neighbouring columns: it is off by up to 2^-11 of itself, or by
+ * 2^-39 of the largest of these terms where that is more, and the sum by the
+ * total of that over its terms, each times |weight|.  Where terms do not cancel
+ * each other or the residual this is an eighth of C's half step; where they do
+ * it can exceed it (take GPTQ_F32 or GPTQ_F16, whose terms are fp32).
  *  H, h_scales      [T·top_k x K] activations by sorted position, row stride
  *                   ldh; rows from offsets[E] on are not read.
  *  ids, weights     [T x top_k]; offsets and order as gptq_moe_plan makes them

@@ -101,10 +101,10 @@ def gated(a, ids, gate, up, kind, grouped=False):
 def combined(h, ids, weights, down, residual, grouped=False, half_terms=False):
     """(y, bound): the sum over j in fp32 loses a rounding for each term, of the
     terms' magnitudes; so does the residual's.  half_terms: the terms are
-    rounded to fp16 on their way, times a power of two for each row and block of
-    128 columns, 2^-(11 + exponent of s), s = Σ|sa·sb| over the blocks of K:
-    half a step is 2^-11 of the term, or 2^-25·2^11·s among fp16's subnormal
-    numbers."""
+    rounded to fp16 on their way, times a power of two for each row of a group
+    of neighbouring columns that divides a block of 128 and that brings the
+    group's largest term to 2^14 .. 2^15: half a step is 2^-11 of the term, or
+    2^-25 of 2^-14 of the largest among fp16's subnormal numbers."""
     T, k = ids.shape
     offsets, order = plan(ids, len(down))
     n = down[0][0].shape[0]
@@ -121,8 +121,7 @@ def combined(h, ids, weights, down, residual, grouped=False, half_terms=False):
         np.add.at(bound, s // k, b * np.abs(w[s])[:, None])
         np.add.at(size, s // k, (np.abs(c) + b) * np.abs(w[s])[:, None])
         if half_terms:
-            scale = np.abs(h[1][rows].astype(np.float64)) @ np.abs(down[e][1].astype(np.float64)).T
-            scale = scale[:, np.arange(n) // fp8.BLOCK]
-            np.add.at(bound, s // k, ((np.abs(c) + b) * 2.0 ** -11 + scale * 2.0 ** -14) * np.abs(w[s])[:, None])
+            top = np.maximum.reduceat(np.abs(c) + b, np.arange(0, n, fp8.BLOCK), axis=1)[:, np.arange(n) // fp8.BLOCK]
+            np.add.at(bound, s // k, ((np.abs(c) + b) * 2.0 ** -11 + top * 2.0 ** -39) * np.abs(w[s])[:, None])
     r = np.zeros((T, n)) if residual is None else np.asarray(residual, dtype=np.float64)
     return y + r, bound + size * 2.0 ** -24 * k + np.abs(y + r) * 2.0 ** -24

@@ -9,9 +9,11 @@
 // into LDS (a copy's addresses are the lanes' own), so no sorted copy of the
 // activations is ever made; the second stores each row's sums at its slot, and
 // one pass adds a token's slots, with their weights, in the order of j.  For
-// bf16 results these sums are rounded to fp16 on their way (kScaled): 2^-11 of
-// each term, an eighth of what the result's own rounding may lose, for half the
-// bytes (4096 tokens, top 8, 2048 columns: 200 -> 153 us).
+// bf16 results these terms are rounded to fp16 on their way (kScaled), for half
+// the bytes (4096 tokens, top 8, 2048 columns: 200 -> 153 us): up to 2^-11 of each
+// term, where the result's own rounding loses up to 2^-8 of the sum.  That is an
+// eighth as long as the terms do not cancel; where they or the residual do, it can
+// be more than the result's half step, and a result in fp32 is the way out.
 #include <cmath>
 
 #include "fp8_tile.hpp"
@@ -22,7 +24,7 @@ namespace {
 // ---------------------------------------------------------------- sum over a token's experts
 // One thread per eight columns of a token.  SCALED: the terms are kScaled's.
 template <int DT, bool SCALED>
-__global__ __launch_bounds__(256) void combine_kernel(const void* P, int64_t nb, const int32_t* ids,
+__global__ __launch_bounds__(256) void combine_kernel(const void* P, int group, const int32_t* ids,
                                                       const float* weights, int64_t T, int64_t N, int k, int E,
                                                       const void* R, int64_t ldr, void* C, int64_t ldc) {
   typedef typename Elem<DT>::type Out;
@@ -31,7 +33,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* P, int64_t nb,
   if (t >= T) return;
   const int c = (int)min((int64_t)8, N - n);
   const _Float16* H = static_cast<const _Float16*>(P);
-  const float* F = reinterpret_cast<const float*>(H + align_scaled(T * k * N));
+  const float* F = reinterpret_cast<const float*>(H + align_scaled(T * k * N)) + (SCALED ? n / group : 0);
+  const int64_t nf = SCALED ? (N + group - 1) / group : 0;
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.f;
@@ -48,7 +51,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* P, int64_t nb,
       if (!on[u]) continue;
       if constexpr (SCALED) {
         load8<GPTQ_F16>(H + s * N + n, c, v[u]);
-        f[u] = F[s * nb + n / 128];
+        f[u] = F[s * nf];
       } else {
         load8<GPTQ_F32>(static_cast<const float*>(P) + s * N + n, c, v[u]);
       }
@@ -626,11 +629,6 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Stream<BM, BN, WM,
       for (int j = 0; j < NI; ++j)
 #pragma unroll
         for (int i = 0; i < MI; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      float ssum[EPI == kScaled ? MI : 1];   // Σ|sa·sb| of each A piece's row
-      if constexpr (EPI == kScaled) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) ssum[i] = 0.f;
-      }
       if (!ready) {
         const char* b = S + (ring % NS) * T::SB;
         const char* sc = S + (half & 1) * T::SCB;
@@ -657,7 +655,6 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Stream<BM, BN, WM,
           sa = sn;
 #pragma unroll
           for (int q = 0; q < NB; ++q) s[q] = sa * sb[q];
-          if constexpr (EPI == kScaled) ssum[i] += fabsf(s[0]);
           if (i + 1 < MI) {
             ra = read_a(b, i + 1);
             sn = *reinterpret_cast<const float*>(sc + soff + (i + 1) * 512);
@@ -718,7 +715,10 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Stream<BM, BN, WM,
       const int l15 = l & 15, nl = wn * WC + 4 * (l >> 4);   // this lane's first column in the tile
       constexpr int NO = GATED ? NI / 2 : NI;
       if constexpr (EPI == kPartial || EPI == kScaled) {
-        // kScaled: P is fp16 [slots][N], behind it the powers of two [slots][nb]
+        // kScaled: P is fp16 [slots][N], behind it the powers of two, one for a row
+        // of the wave's columns
+        constexpr int GROUP = WC;
+        const int64_t nf = (a.N + GROUP - 1) / GROUP;
         _Float16* P = reinterpret_cast<_Float16*>(a.P);
         float* F = reinterpret_cast<float*>(P + align_scaled((int64_t)a.slots * a.N));
         // kPartial: sixteen rows at a time go through LDS, so that neighbouring
@@ -729,16 +729,43 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Stream<BM, BN, WM,
         constexpr int U = WN / 4, PIECE = 16 * U * 16, TURNS = 2 * PIECE <= T::PER * 1024 ? 2 : 1;
         static_assert(PIECE <= T::PER * 1024 && T::SEGS % T::WAVES == 0, "place for a piece of sums");
         char* mine = S + ((ring + nst + NS - 1) % NS) * T::SB + w * T::PER * 1024;
+        // kScaled: each row's largest (columns that do not exist hold another
+        // column's sums).  x + 0·x is x, and NaN where x is infinite.
+        float most[EPI == kScaled ? MI : 1];
+        if constexpr (EPI == kScaled) {
+          bool beyond = false;
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            most[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+              most[i] = largest(most[i], acc[j][i][0], acc[j][i][1]);
+              most[i] = largest(most[i], acc[j][i][2], acc[j][i][3]);
+            }
+            beyond |= most[i] == kInfinity;
+          }
+          if (__builtin_expect(__ballot(beyond) != 0, 0)) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+              most[i] = 0.f;
+#pragma unroll
+              for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; r += 2)
+                  most[i] = largest(most[i], __builtin_fmaf(acc[j][i][r], 0.f, acc[j][i][r]),
+                                    __builtin_fmaf(acc[j][i][r + 1], 0.f, acc[j][i][r + 1]));
+            }
+          }
+        }
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
           if constexpr (EPI == kScaled) {
             const int ml = wm * WM + i * 16 + l15;
             const int64_t row = slots_[tab][ml];
             const bool there = ml < cur.mleft && row >= 0 && row < a.slots;
-            const int e = scaled_exponent(ssum[i]);
+            const int e = scaled_exponent(quarters_max(__builtin_bit_cast(uint32_t, most[i])));
             const float f = power_of_two(-e);
-            if (there && lane < 16 && (wn * WC) % 128 == 0 && nl < nleft)
-              F[row * a.nb + (cur.n0 + nl) / 128] = power_of_two(e);
+            if (there && lane < 16 && nl < nleft) F[row * nf + (cur.n0 + nl) / GROUP] = power_of_two(e);
 #pragma unroll
             for (int j = 0; j < NI; ++j)
 #pragma unroll
@@ -853,6 +880,7 @@ int64_t most_stretches(int64_t slots, int64_t E, int64_t bm) {
 template <int BM, int BN, int WM, int WN, int NS, bool FAST, int FORM, int EPI, int DT, int ROWS, bool FLOW = false>
 hipError_t launch_tiles(GArgs& a, hipStream_t s) {
   a.tn = (int)ceil_div(a.N, FORM == kGated ? BN / 2 : BN);
+  a.group = WN;
   const int64_t most = most_stretches(a.slots, a.E, BM) * a.tn;
   if (most > INT32_MAX) return hipErrorInvalidValue;
   // FLOW: as many workgroups as run at once (a multiple of 8: each stays with its XCD's tiles)
@@ -958,9 +986,9 @@ size_t fp8_expert_gated_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t N) {
 }
 size_t fp8_expert_gemm_ws_bytes(int64_t T, int64_t k, int64_t N) {
   if (T <= kTokens && T * k <= kTokenSlots) return 256;
-  // fp32 terms, or fp16 ones with a power of two for each block of columns
+  // fp32 terms, or fp16 ones with a power of two for each 32 columns or 64
   const int64_t n = T * k * N;
-  return std::max<size_t>(512, align_up((size_t)std::max(n * 4, align_scaled(n) * 2 + T * k * ceil_div(N, 128) * 4)));
+  return std::max<size_t>(512, align_up((size_t)std::max(n * 4, align_scaled(n) * 2 + T * k * ceil_div(N, 32) * 4)));
 }
 
 hipError_t fp8_expert_gated_launch(const uint8_t* A, const float* sa, int64_t T, int64_t K, int64_t lda,
@@ -1029,7 +1057,7 @@ hipError_t fp8_expert_gemm_launch(const uint8_t* A, const float* sa, int64_t T, 
   if (e != hipSuccess) return e;
   const int64_t grid = ceil_div(T * ceil_div(N, 8), 256);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-#define GQ_SUM(DT, SC) combine_kernel<DT, SC><<<(unsigned)grid, 256, 0, s>>>(a.P, a.nb, ids, weights, T, N, k, E, R, ldr, C, ldc)
+#define GQ_SUM(DT, SC) combine_kernel<DT, SC><<<(unsigned)grid, 256, 0, s>>>(a.P, a.group, ids, weights, T, N, k, E, R, ldr, C, ldc)
   if (c_dt == GPTQ_F32) GQ_SUM(GPTQ_F32, false);
   else if (c_dt == GPTQ_F16) GQ_SUM(GPTQ_F16, false);
   else GQ_SUM(GPTQ_BF16, true);

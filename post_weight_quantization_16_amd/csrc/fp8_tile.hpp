@@ -56,6 +56,7 @@ struct GArgs {
   const int32_t* offsets; const int32_t* order;
   int E, topk, slots;
   int64_t next[2];   // bytes from an expert's weights to the next one's
+  int group;         // kScaled: columns that share a power of two
 };
 
 // What is computed: C = A·Bᵀ, act(A·Gᵀ)·(A·Uᵀ), act(A·Bᵀ + bias) + residual.
@@ -325,6 +326,18 @@ __device__ __forceinline__ void put1(void* p, int dt, int64_t at, float x) {
   else if (dt == GPTQ_BF16) static_cast<__bf16*>(p)[at] = (__bf16)x;
   else static_cast<_Float16*>(p)[at] = (_Float16)x;
 }
+// The largest of the four values that lanes 16 apart hold, in all of them.
+__device__ __forceinline__ uint32_t quarters_max(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
+}
+// The largest of m, |a| and |b|, without what is NaN.
+__device__ __forceinline__ float largest(float m, float a, float b) {
+  asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(a), "v"(b));
+  return m;
+}
 // Magnitudes as integers: finite < infinity < NaN.
 __device__ __forceinline__ uint32_t mag_bits(float x) {
   return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
@@ -394,18 +407,17 @@ __device__ __forceinline__ void tile_of(uint32_t L, uint32_t total, uint32_t tm,
 }
 
 // Results as they are, fp32 sums to be joined, codes; and sums for bf16 results
-// in fp16, each row of a block of columns times a power of two of its own.
+// in fp16, each row of a group of columns times a power of two of its own.
 enum { kStore = 0, kPartial = 1, kCodes = 2, kScaled = 3 };
 
-// The power of two for kScaled, from s = Σ|sa·sb| over the row's blocks: codes
-// are 448 at most, so a sum is below s·128·448² < s·2^24.63 and, times 2^-(11 +
-// exponent of s), below 2^14.63: fp16 holds it.  Usual sums are 2^9 to 2^12
-// smaller, still 2^15 above the last normal number of fp16.  The limits keep the
-// power an fp32 number; beyond the upper one fp32's own largest sum, times
-// 2^-124, is 2^4.
-__device__ __forceinline__ int scaled_exponent(float s) {
-  return min(max((int)((__builtin_bit_cast(uint32_t, s) >> 23) & 0xFF) - 127, -126), 113) + 11;
-}
+// The power of two for kScaled, from the largest finite magnitude of a row's sums
+// over a group of columns (the wave's own; an infinity beside them shall not take
+// theirs): that one comes to 2^14 .. 2^15, which fp16 holds, and all down to 2^-28 of it keep fp16's 11 bits; below, half a step
+// is 2^-39 of it.  (A bound of the sums from their scales instead would take the
+// bits of those whose codes are small.)  The limit keeps the power's reciprocal
+// an fp32 number; fp32's smallest sums then come to 2^-23 and more.
+__device__ __forceinline__ int scaled_exponent(uint32_t mag) { return max((int)(mag >> 23) - 127 - 14, -126); }
+constexpr float kInfinity = __builtin_inff();
 __device__ __forceinline__ float power_of_two(int e) {
   return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
 }
