@@ -300,7 +300,7 @@ __global__ __launch_bounds__(WAVES * 64) void few_gated_kernel(GArgs a) {
   for (int e = t; e <= a.E; e += WAVES * 64) offs[e] = offset_of(a, e);
   __syncthreads();
   const uint32_t u = blockIdx.x / (uint32_t)a.tn;
-  const Stretches<8> all(offs, a.E);
+  const Stretches<8> all(offs, a.E, a.slots);
   if (u >= (uint32_t)all.total) return;
   const int64_t n0 = (int64_t)(blockIdx.x - u * a.tn) * 16;
   const Stretch s = all.find(offs, a.E, __builtin_amdgcn_readfirstlane((int)u));
@@ -444,7 +444,7 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Stream<BM, BN, WM,
   const int wm = w / (BN / WN), wn = w % (BN / WN);
   for (int e = t; e <= a.E; e += T::NT) offs[e] = offset_of(a, e);
   __syncthreads();
-  const Stretches<BM> all(offs, a.E);
+  const Stretches<BM> all(offs, a.E, a.slots);
   const uint32_t tiles = (uint32_t)all.total * a.tn;
   if (blockIdx.x >= tiles) return;
   struct Where { int e, m0, mleft, n0; };
@@ -872,16 +872,11 @@ __global__ __launch_bounds__((Tile<BM, BN, WM, WN, NS>::NT), (Stream<BM, BN, WM,
 }
 
 // ---------------------------------------------------------------- launch
-// The most stretches of BM rows that `slots` rows of E experts can make.
-int64_t most_stretches(int64_t slots, int64_t E, int64_t bm) {
-  return std::min(slots, slots / bm + std::min(E, slots));
-}
-
 template <int BM, int BN, int WM, int WN, int NS, bool FAST, int FORM, int EPI, int DT, int ROWS, bool FLOW = false>
 hipError_t launch_tiles(GArgs& a, hipStream_t s) {
   a.tn = (int)ceil_div(a.N, FORM == kGated ? BN / 2 : BN);
   a.group = WN;
-  const int64_t most = most_stretches(a.slots, a.E, BM) * a.tn;
+  const int64_t most = most_stretches<int64_t>(a.slots, a.E, BM) * a.tn;
   if (most > INT32_MAX) return hipErrorInvalidValue;
   // FLOW: as many workgroups as run at once (a multiple of 8: each stays with its XCD's tiles)
   const unsigned grid = (unsigned)(FLOW ? std::min<int64_t>(most, 256 * Stream<BM, BN, WM, WN, NS, EPI, FLOW>::FIT) : most);
@@ -931,7 +926,7 @@ template <int EPI, int DT> hipError_t run_gated(GArgs& a, hipStream_t s) {
   if (few_gated(a.slots, a.E, a.topk, a.N) && (EPI != kCodes || a.P)) {
     constexpr int E = EPI == kCodes ? kPartial : kStore;
     a.tn = (int)ceil_div(a.N, 16);
-    const unsigned grid = (unsigned)(most_stretches(a.slots, a.E, 8) * a.tn);
+    const unsigned grid = (unsigned)(most_stretches<int64_t>(a.slots, a.E, 8) * a.tn);
     if (grid <= 256) few_gated_kernel<FAST, E, 8><<<grid, 512, 0, s>>>(a);
     else few_gated_kernel<FAST, E, 4><<<grid, 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();

@@ -426,17 +426,26 @@ __device__ __forceinline__ float power_of_two(int e) {
 // The sorted positions in stretches of up to BM rows of one expert, numbered
 // along the order.  Found by every wave for itself: lane l counts the stretches
 // of experts l·per .. (l+1)·per - 1, and a scan over the lanes gives what lies
-// before them.  Offsets are clamped to the slots there are, so that no table
-// makes a kernel read outside its rows.
+// before them.  Offsets are clamped to the slots there are, and the counts to the
+// most stretches that sorted slots can make (most_stretches; the grid is made for
+// them), so that no table makes a kernel read outside its rows or a count pass 32
+// bits: offsets that go up and down over 2^30 slots of 1024 experts would count
+// 2^32 stretches of 128.  Sums that saturate leave no stretch below the total
+// without a lane that finds it.
 struct Stretch { int expert, row, rows; };
 __device__ __forceinline__ int offset_of(const GArgs& a, int e) {
   return min(max(a.offsets[min(e, a.E)], 0), a.slots);
 }
+// The most stretches of bm rows that `slots` rows of E experts can make.
+template <typename T> __host__ __device__ __forceinline__ T most_stretches(T slots, T E, T bm) {
+  const T n = slots / bm + (E < slots ? E : slots);
+  return n < slots ? n : slots;
+}
 template <int BM> struct Stretches {
   int per, e0, sum, below, total;
   // offsets: clamped, [E + 1]
-  __device__ __forceinline__ Stretches(const int* offsets, int E) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ Stretches(const int* offsets, int E, int slots) {
+    const int lane = threadIdx.x & 63, most = most_stretches(slots, E, BM);
     per = (E + 63) >> 6;
     e0 = lane * per;
     sum = 0;
@@ -444,14 +453,14 @@ template <int BM> struct Stretches {
 #pragma unroll 1
     for (int j = 1; j <= per; ++j) {
       const int p = offsets[min(e0 + j, E)];
-      sum += max(p - o + BM - 1, 0) / BM;
+      sum = min(sum + max(p - o + BM - 1, 0) / BM, most);
       o = p;
     }
     int in = sum;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
       const int y = __shfl_up(in, d);
-      if (lane >= d) in += y;
+      if (lane >= d) in = min(in + y, most);
     }
     below = in - sum;
     total = __builtin_amdgcn_readlane(in, 63);
