@@ -10,10 +10,9 @@ namespace {
 // The kernel for a product is the one that this model says is quickest.  Its
 // times are microseconds on MI355X (fp8 instructions / exact form): a stage of a
 // tile with one workgroup on each of the 256 CUs, and with as many as fit; a
-// round's start and epilogue.  Fitted to every kernel and split of 240 products
-// of random sizes (M to 2900, K to 10 944): what it picks takes 0.7 % longer
-// than the quickest on average, a third longer at worst (40 x 5760 x 1216: few
-// rows 10.0, 32-tiles 7.3).  Small tiles win
+// round's start and epilogue.  Fitted to every kernel and split of 240 plain and
+// gated products of random sizes (M to 2900, K to 10 944), of which 40 x 5760 x
+// 1216 was missed by most (few rows 10.0, 32-tiles 7.3).  Small tiles win
 // where there are few (512 x 4096: 64-tiles 18.7 / 29.1 us, 128-tiles in two
 // splits 25.2 / 31.3, 256-tiles in eight 39 / 45), large ones where there are
 // many (4096 x 4096: 131 / 201, 83 / 140, 67 / 118).
@@ -32,6 +31,15 @@ constexpr double kLaunch = 2.7, kJoin = 2.2, kJoinLoads = 0.5, kJoinBytes = 4.0e
 // cycles a block and wave: conversions, products, the rest), or all weights
 // from memory (KB a us).
 constexpr double kFewLaunch = 1.8, kFewGroup = 1.3, kFewCopies = 81.0, kFewWeights = 7e3, kClock = 2100.0;
+// Its codes without a gate: sums go to memory 64 bytes of a row at a time, 16 rows
+// and columns a store, and back (us, bytes per us).  Fitted to 176 products of 9 to
+// 64 rows by 16 weights from 1024 x 4096 to 20480 x 5120 with all kernels timed
+// (what is picked takes 0.7 % longer than the quickest on average, 10 % at worst;
+// with the gated products' kJoin 3.0 and 28, 48 x 16384 x 2048: few rows 21.8, 64-
+// tiles in two splits 17.0) and tried on 144 others, of random sizes, 1 to 64 rows
+// by 512 to 20000 x 256 to 12000: 2.8 %, 38 at worst (14 x 17449 x 278: tiles of
+// 128 rows 14.8, of 32 10.7); with kJoin 3.7.
+constexpr double kFewJoin = 1.2, kFewJoinBytes = 7.5e5;
 
 struct Plan { int tile; int splits, kper; };   // tile -1: few rows
 
@@ -55,12 +63,10 @@ inline Plan search_plan(int64_t M, int64_t N, int64_t K, bool gated, bool exact,
     const double copied = 2.0 * kb * (nb + (M <= 8 ? 0.5 : mt)) / kFewCopies;
     const double cycles = exact ? 92 * (nb + mt) + 115 * nb * mt + 65 : 48 * nb * mt + 200;
     const double issued = 2.0 * (double)ceil_div(kb, waves) * cycles / kClock;
-    least = kFewLaunch + (codes ? kJoin : 0) +
+    const double join = !codes ? 0 : gated ? kJoin : kFewJoin + (double)M * N * 8 / kFewJoinBytes;
+    least = kFewLaunch + join +
             std::max((double)ceil_div(groups, 256 * here) * (kFewGroup + here * std::max(copied, issued)),
                      2.0 * groups * kb * nb / kFewWeights);
-    // codes without a gate: three 32-column tiles' conversions and more take
-    // longer than that (37 x 11008 x 4000: 27 us, 32 x 64 tiles in two splits 22)
-    if (codes && !gated && mt >= 3) least *= 1.15;
     best = {-1, 1, (int)kb};
   }
   for (int i = 0; i < kTileKinds; ++i) {

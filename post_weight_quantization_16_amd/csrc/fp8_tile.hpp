@@ -933,7 +933,10 @@ __global__ __launch_bounds__((Few<NA, FORM == kGated>::WAVES * 64)) void few_row
       for (int i = 0; i < F::PER; ++i)
         lds_copy16(rbase + (unsigned)dest(slot, i), base(i) + (int64_t)(kbeg + j) * 128, voff[i]);
     } else if (FORM == kLinear && a.wide && a.K % 16 == 0) {
-      // K ends between two pieces (37 x 11008 x 4000 to codes 22.5 us, through registers 25.9)
+      // K ends between two pieces (to codes, us, in brackets through registers, at 8 / 33
+      // / 64 rows: 11008 x 4000 13.7 (15.4) / 24.9 (28.6) / 31.6 (33.5), 9000 x 1504 9.1
+      // (10.0) / 15.7 (19.7) / 19.0 (24.1), 1024 x 5392 8.6 (8.5) / 11.2 (11.1) / 13.4
+      // (13.4)).  The plain and gated products' kernels are without it.
 #pragma unroll
       for (int i = 0; i < F::PER; ++i) {
         const int p16 = (((lane & 7) ^ (lane >> 4)) << 4) ^ ((i & 1) << 6);
