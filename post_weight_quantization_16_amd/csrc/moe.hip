@@ -16,6 +16,7 @@
 // Bound: latency.  The logits of 16384 tokens over 128 experts are 4 MB, less
 // than a microsecond of the memory's time.
 #include "fp8.hpp"
+#include "route_plan.hpp"
 
 namespace gq {
 namespace {
@@ -259,7 +260,6 @@ template <int DT, int V> __device__ __forceinline__ void logits_of(const void* X
 // SCORED: the choice needs p (a bias, or groups by their best two); otherwise
 // the keys are the logits, in fp32, which holds them exactly.
 // ONE: one block routes all tokens and sorts their slots too.
-constexpr int route_threads(int L, int V) { return L * V <= 256 && V <= 8 ? 1024 : 256; }
 template <int L, int V, bool SCORED, bool ONE>
 __global__ __launch_bounds__(route_threads(L, V)) void route_kernel(RouteArgs a) {
   typedef typename KeyOf<SCORED>::type Key;
@@ -460,37 +460,12 @@ __global__ __launch_bounds__(route_threads(L, V)) void route_kernel(RouteArgs a)
   }
 }
 
-constexpr int kMaxBlocks = 256;   // rows of hist: every sorting block reads them all
-
-// How T tokens are routed.
-struct RoutePlan { int lanes, v, threads, per, blocks; bool one; size_t lds; };
-constexpr int64_t kFewTokens = 2048;   // up to here a token gets a wave
-RoutePlan route_plan(int64_t T, int E, int k, int groups) {
-  RoutePlan p;
-  const bool one_lanes = T <= 64 && E <= 128 && groups == 1;   // one block does it all
-  p.lanes = E <= 128 && T > (one_lanes ? 16 : kFewTokens) ? 16 : 64;
-  p.v = 1;
-  while (p.v * p.lanes < E) p.v *= 2;
-  // blocks of 16 waves where one then does it all, or 256 of them fill the
-  // card; with 16 lanes a token, groups' keys leave LDS for 4
-  p.threads = 256;
-  if (route_threads(p.lanes, p.v) == 1024 && (groups == 1 || p.lanes == 64) &&
-      (T > kMaxBlocks * (256 / p.lanes) || (T > 256 / p.lanes && T <= 1024 / p.lanes)))
-    p.threads = 1024;
-  const int here = p.threads / p.lanes;
-  p.one = T <= here;
-  p.per = (int)(ceil_div(ceil_div(T, kMaxBlocks), here) * here);
-  p.blocks = (int)ceil_div(T, std::max(p.per, 1));
-  p.lds = (size_t)here * k * 12 + (groups > 1 ? (size_t)here * (E + 2 * p.lanes) * 8 : 0) + (size_t)E * 4;
-  if (p.one) p.lds = std::max(p.lds, (size_t)E * (2 + p.threads / 64) * 4);
-  return p;
-}
-
 template <bool SCORED, bool ONE> hipError_t launch_route(const RouteArgs& a, const RoutePlan& p, hipStream_t s) {
 #define GQ_ROUTE(L, V) \
   if (p.lanes == L && p.v == V) route_kernel<L, V, SCORED, ONE><<<ONE ? 1 : p.blocks, p.threads, p.lds, s>>>(a)
-  GQ_ROUTE(16, 1); GQ_ROUTE(16, 2); GQ_ROUTE(16, 4); GQ_ROUTE(16, 8); GQ_ROUTE(16, 16);
-  GQ_ROUTE(64, 1); GQ_ROUTE(64, 2); GQ_ROUTE(64, 4); GQ_ROUTE(64, 8); GQ_ROUTE(64, 16);
+  GQ_ROUTE(16, 1); else GQ_ROUTE(16, 2); else GQ_ROUTE(16, 4); else GQ_ROUTE(16, 8);
+  else GQ_ROUTE(64, 1); else GQ_ROUTE(64, 2); else GQ_ROUTE(64, 4); else GQ_ROUTE(64, 8); else GQ_ROUTE(64, 16);
+  else return hipErrorInvalidValue;
 #undef GQ_ROUTE
   return hipGetLastError();
 }
