@@ -943,7 +943,7 @@ def moe_plan(ids, weights, n_experts: int, ws=None) -> Routing:
 
 def fp8_quantize_experts(W, out: Fp8Experts | None = None) -> Fp8Experts:
     """W [E, N, K] (float32/bfloat16/float16) in e4m3, each expert's matrix as
-    fp8_quantize(W[e], 128) gives it."""
+    fp8_quantize(W[e], 128) gives it.  out: to be filled; its experts lie apart."""
     if W.dim() != 3:
         raise ValueError("W must be [E, N, K]")
     empty, e4m3, f32 = _t8()[:3]
@@ -955,10 +955,21 @@ def fp8_quantize_experts(W, out: Fp8Experts | None = None) -> Fp8Experts:
                                dtype=f32, device=W.device))
     elif out.codes.shape != W.shape or out.codes.device != W.device:
         raise ValueError(f"out must have shape {tuple(W.shape)} on {W.device}")
-    _experts_arg(out, "out", W.device)
+    _, _, _, ld, next_ = _experts_arg(out, "out", W.device)
+    if _experts_overlap(E, N, K, ld, next_):
+        raise ValueError("out's experts overlap in memory")
     for e in range(E):
         fp8_quantize(W[e], FP8_BLOCK, out=out.expert(e))
     return out
+
+
+def _experts_overlap(E, N, K, ld, next_) -> bool:
+    """Whether rows of two experts share bytes (one's rows lie apart: ld >= K)."""
+    for e in range(1, E):
+        n = e * next_ // max(ld, 1)   # the other's rows next to this one's first
+        if any(abs(e * next_ - min(i, N - 1) * ld) < K for i in (n, n + 1)):
+            return True
+    return False
 
 
 def _experts_arg(m: Fp8Experts, name, device):
