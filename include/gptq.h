@@ -591,7 +591,10 @@ int gptq_moe_plan(const int32_t* ids, int64_t T, int top_k, int64_t n_experts, i
  * for the sorted positions i (expert e, token t).  Rows from offsets[E] on are
  * left as they were.  Products, activation and codes as in
  * gptq_fp8_gated_gemm: exact with fp32 sums for GPTQ_F32 and for codes.
- *  A, a_scales      [T x K] activations, row stride lda.
+ *  A, a_scales      [T x K] activations, row stride lda.  Beyond T * lda = 2^31
+ *                   bytes loads go through registers, as for rows that do not
+ *                   start at multiples of 16 bytes: 270 000 tokens of 8192 took
+ *                   3.6 times as long a token as 250 000 (split such a batch).
  *  G, g_scales, ldg, next_g   [E][N x K] gate weights: rows ldg bytes apart,
  *                   experts next_g bytes (>= 0); scales dense, [E][ceil(N/128) x
  *                   ceil(K/128)].  U, u_scales, ldu, next_u: up weights.
@@ -627,7 +630,9 @@ int gptq_fp8_expert_gated_gemm(const uint8_t* A, const float* a_scales, int64_t 
  *  R, ld_r          residual [T x N] of c_dtype or NULL; may be C itself (same
  *                   address and stride), else must not overlap it.
  *  C, c_dtype, ldc  out [T x N].
- *  ws               of GPTQ_WS_EXPERT_GEMM; required where that is not 256. */
+ *  ws               of GPTQ_WS_EXPERT_GEMM; required where that is not 256.  Its
+ *                   size, 4 bytes for each slot and column (GPTQ_BF16 uses half),
+ *                   is for any c_dtype. */
 int gptq_fp8_expert_gemm(const uint8_t* H, const float* h_scales, int64_t T, int64_t K, int64_t ldh,
                          int top_k, const int32_t* ids, const float* weights, const int32_t* offsets,
                          const int32_t* order, int64_t n_experts, const uint8_t* D,

@@ -943,7 +943,8 @@ def moe_plan(ids, weights, n_experts: int, ws=None) -> Routing:
 
 def fp8_quantize_experts(W, out: Fp8Experts | None = None) -> Fp8Experts:
     """W [E, N, K] (float32/bfloat16/float16) in e4m3, each expert's matrix as
-    fp8_quantize(W[e], 128) gives it.  out: to be filled; its experts lie apart."""
+    fp8_quantize(W[e], 128) gives it, one call for each.  out: to be filled; its
+    experts lie apart."""
     if W.dim() != 3:
         raise ValueError("W must be [E, N, K]")
     empty, e4m3, f32 = _t8()[:3]

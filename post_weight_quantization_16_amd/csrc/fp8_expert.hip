@@ -86,6 +86,12 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* P, int group, 
 //   top 2 of 8, 4096 x 11008     19.0 (54.6)   53.8 (73.7)   90.0 (97.7)
 //   top 8 of 256, 4096 x 512      7.7 (16.2)   15.1 (23.4)   42.6 (52.9)
 //   top 4 of 16, 1024 x 4096      9.0 (25.4)   16.6 (25.8)   25.0 (26.0)
+// From 8 tokens on the two are near each other and the tiles, with more waves for
+// the same bytes, can win (8 / 9 / 12 / 16 tokens of two other runs: top 8 of 128, 2048
+// x 768, 20.6 (27.0), 24.4 (27.7), 30.4 (31.9), 35.6 (35.7); top 4 of 128, 2880 x 2880,
+// 63.8 (62.3), 70.9 (59.2), 76.2 (71.3), 89.7 (84.4)); the bound is one number all
+// the same, so that a token's result does not change its terms' type with the size
+// of the weights.
 constexpr int kTokens = 16, kTokenSlots = 128;
 
 // WAVES: 8, or 16 where there are few columns (16 tokens, top 4 of 16, 1024 x
@@ -411,10 +417,18 @@ __global__ __launch_bounds__(WAVES * 64) void few_gated_kernel(GArgs a) {
 // The slots of a tile's rows come with copies of 4 bytes a lane like the scales;
 // three tables of them, for the wave that still stores the tile before, this
 // tile and the next.
-// FLOW: that; otherwise one tile a workgroup.  A stage of a stream is up to a
-// tenth slower (more scalars than there are registers for), so long products go
-// without: 4096 x 11008 over 8 experts of 1024 rows 519 us without, 550 with it;
-// 4096 x 512 over 256 experts of 32 rows 199 and 172, of 128 rows 398 and 322.
+// FLOW: that; otherwise one tile a workgroup.  A stage of a stream is slower (more
+// scalars than there are registers for), so long products go without.  With a
+// stream / without, to bf16, us by blocks of K:
+//   experts, rows, columns   4             8             12            20            48
+//   64 of 24, 2048           24.5 / 26.3   35.6 / 35.9   53.1 / 52.9   84.9 / 81.6   176 / 173
+//   64 of 128, 2048          46.9 / 49.9   66.9 / 69.8   88.8 / 89.9   131 / 130     253 / 243
+//   16 of 200, 4096          36.3 / 36.9   43.6 / 44.1   53.2 / 52.7   78.2 / 75.5   150 / 151
+//   64 of 512, 2048          126 / 130     175 / 175     229 / 224     317 / 315     613 / 591
+//   16 of 512, 4096          69.3 / 70.1   89.7 / 87.8   116 / 113     168 / 160     335 / 319
+// Tiles of 32 rows, which wait for the weights, stream at any length: between 6 %
+// less and 5 % more.
+constexpr int kFlowBlocks = 10;
 template <int BM, int BN, int WM, int WN, int NS, int EPI, bool FLOW> struct Stream {
   using T = Tile<BM, BN, WM, WN, NS>;
   static constexpr int ROWS = BM < 64 ? 64 : BM;   // of a table: a copy fills 64
@@ -964,11 +978,11 @@ template <bool FAST, int EPI> hipError_t run_sorted(GArgs& a, hipStream_t s) {
   const bool few = r <= 112 && std::min(a.slots, a.E) * ceil_div(a.N, 256) <= 64;
   if (r < 48 || few) return launch_tiles<32, 128, 32, 32, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, true>(a, s);
   if (!FAST || r < 300) {
-    if (a.kb > 20) return launch_tiles<128, 256, 64, 64, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, false>(a, s);
+    if (a.kb > kFlowBlocks) return launch_tiles<128, 256, 64, 64, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, false>(a, s);
     return launch_tiles<128, 256, 64, 64, 3, FAST, kPlain, EPI, GPTQ_F32, kSorted, true>(a, s);
   }
   if constexpr (FAST) {
-    if (a.kb > 20) return launch_tiles<256, 256, 128, 64, 2, FAST, kPlain, EPI, GPTQ_F32, kSorted, false>(a, s);
+    if (a.kb > kFlowBlocks) return launch_tiles<256, 256, 128, 64, 2, FAST, kPlain, EPI, GPTQ_F32, kSorted, false>(a, s);
     return launch_tiles<256, 256, 128, 64, 2, FAST, kPlain, EPI, GPTQ_F32, kSorted, true>(a, s);
   }
   return hipErrorInvalidValue;
