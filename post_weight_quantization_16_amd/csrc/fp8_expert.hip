@@ -10,7 +10,7 @@
 // activations is ever made; the second stores each row's sums at its slot, and
 // one pass adds a token's slots, with their weights, in the order of j.  For
 // bf16 results these terms are rounded to fp16 on their way (kScaled), for half
-// the bytes (4096 tokens, top 8, 2048 columns: 200 -> 153 us): up to 2^-11 of each
+// the bytes (4096 tokens, top 8, 2048 columns: 201 -> 156 us): up to 2^-11 of each
 // term, where the result's own rounding loses up to 2^-8 of the sum.  That is an
 // eighth as long as the terms do not cancel; where they or the residual do, it can
 // be more than the result's half step, and a result in fp32 is the way out.
