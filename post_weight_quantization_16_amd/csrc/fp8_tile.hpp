@@ -412,10 +412,11 @@ enum { kStore = 0, kPartial = 1, kCodes = 2, kScaled = 3 };
 
 // The power of two for kScaled, from the largest finite magnitude of a row's sums
 // over a group of columns (the wave's own; an infinity beside them shall not take
-// theirs): that one comes to 2^14 .. 2^15, which fp16 holds, and all down to 2^-28 of it keep fp16's 11 bits; below, half a step
-// is 2^-39 of it.  (A bound of the sums from their scales instead would take the
-// bits of those whose codes are small.)  The limit keeps the power's reciprocal
-// an fp32 number; fp32's smallest sums then come to 2^-23 and more.
+// their bits): that one comes to 2^14 .. 2^15, which fp16 holds, and all down to
+// 2^-28 of it keep fp16's 11 bits; below, half a step is 2^-39 of it.  (A bound of
+// the sums from their scales instead would take the bits of those whose codes are
+// small.)  The limit keeps the power's reciprocal an fp32 number; fp32's smallest
+// sums then come to 2^-23 and more.
 __device__ __forceinline__ int scaled_exponent(uint32_t mag) { return max((int)(mag >> 23) - 127 - 14, -126); }
 constexpr float kInfinity = __builtin_inff();
 __device__ __forceinline__ float power_of_two(int e) {
